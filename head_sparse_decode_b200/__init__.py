@@ -511,6 +511,198 @@ def sha_selective_mlp(x, W1t, W2t, S, n_S, y=None, activation="relu", workspace=
     return y
 
 
+_i64x2 = ctypes.c_int64 * 2
+_f = ctypes.c_float
+_lib.sha_rope.argtypes = [_vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _vp, _vp, _vp, _i, _vp]
+_lib.sha_rope.restype = _i
+_lib.sha_append_paged.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _i, _i,
+                                  _i, _i, _vp, _i, _i, _f, _vp, _vp, _i, _vp, _vp, _i, _vp]
+_lib.sha_append_paged.restype = _i
+
+
+def _on_device(device, entry, *args, stream=None):
+    """entry(*args, stream) with `device` current; raises on an error status.  The
+    device is switched only if it is not the current one already."""
+    handle = _stream_handle(stream, device)
+    if device.index == torch.cuda.current_device():
+        _check(entry(*args, handle))
+    else:
+        with torch.cuda.device(device):
+            _check(entry(*args, handle))
+
+
+def _check_heads_view(name, t, like=None):
+    """A [T, H, d] CUDA view with d contiguous, of `like`'s dtype and device."""
+    if t.dim() != 3 or not t.is_cuda or (t.stride(2) != 1 and t.shape[2] > 1):
+        raise ValueError(f"{name} must be a CUDA tensor [T, H, d] with d contiguous")
+    if like is not None:
+        if t.device != like.device:
+            raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+        if t.dtype != like.dtype:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected {like.dtype}")
+
+
+def _check_vector(name, t, length, dtype, device):
+    if t.dim() != 1 or t.shape[0] != length or t.dtype != dtype or not t.is_contiguous() \
+            or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} [{length}] tensor on {device}")
+
+
+def _check_inv_freq(inv_freq, device):
+    if inv_freq.dim() != 1 or inv_freq.dtype != torch.float64 or not inv_freq.is_contiguous() \
+            or inv_freq.device != device:
+        raise ValueError(f"inv_freq must be a contiguous float64 [rotary/2] tensor on {device}")
+
+
+def rope_frequencies(rotary, base=10000.0, scaling=None, device=None):
+    """The tables of a rotary embedding: (inv_freq float64 [rotary/2], mscale).
+
+    Pair i turns by base^(-2i/rotary) radians per position.  ``scaling`` stretches
+    that to contexts longer than the trained ``original_length`` by ``factor``:
+
+      None
+      {"kind": "linear", "factor": f}                   every frequency divided by f
+      {"kind": "ntk", "factor": f}                      base * f^(rotary/(rotary-2))
+      {"kind": "bands", "factor": f, "original_length": n, "low": 1, "high": 4}
+          pairs that turn fewer than `low` times within n tokens divided by f, those
+          that turn more than `high` times kept, a linear blend in turns between
+          (LLaMA-3.1's rule)
+      {"kind": "yarn", "factor": f, "original_length": n, "fast": 32, "slow": 1,
+       "mscale": 0.1 ln f + 1}
+          kept where a pair turns more than `fast` times within n tokens, divided by
+          f below `slow` turns, a linear blend in the pair index between; mscale
+          multiplies cos and sin
+    """
+    rotary = int(rotary)
+    if rotary < 2 or rotary % 2:
+        raise ValueError("rotary must be even and at least 2")
+    if not base > 1.0:
+        raise ValueError("base must be above 1")
+    scaling = dict(scaling) if scaling else {"kind": "none"}
+    kind = scaling.pop("kind", None)
+    allowed = {"none": (), "linear": ("factor",), "ntk": ("factor",),
+               "bands": ("factor", "original_length", "low", "high"),
+               "yarn": ("factor", "original_length", "fast", "slow", "mscale")}
+    if kind not in allowed:
+        raise ValueError(f"unknown scaling kind {kind!r}")
+    for key in scaling:
+        if key not in allowed[kind]:
+            raise ValueError(f"scaling {kind!r} takes no {key!r}")
+    for key in allowed[kind][:2]:
+        if not scaling.get(key, 0) > 0:
+            raise ValueError(f"scaling {kind!r} needs a positive {key!r}")
+    f = float(scaling.get("factor", 1.0))
+    if kind == "ntk":
+        if rotary == 2:
+            raise ValueError("scaling 'ntk' needs rotary > 2")
+        base = base * f ** (rotary / (rotary - 2))
+    i = torch.arange(rotary // 2, dtype=torch.float64)
+    freq = base ** (-2.0 * i / rotary)
+    mscale = 1.0
+    if kind == "linear":
+        freq = freq / f
+    elif kind == "bands":
+        low, high = float(scaling.get("low", 1.0)), float(scaling.get("high", 4.0))
+        if not high > low:
+            raise ValueError("scaling 'bands' needs high > low")
+        turns = scaling["original_length"] * freq / (2.0 * math.pi)
+        keep = ((turns - low) / (high - low)).clamp(0.0, 1.0)
+        freq = freq * keep + freq / f * (1.0 - keep)
+    elif kind == "yarn":
+        n = float(scaling["original_length"])
+
+        def pair_at(turns):
+            return rotary * math.log(n / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
+
+        lo = max(math.floor(pair_at(float(scaling.get("fast", 32.0)))), 0)
+        hi = min(math.ceil(pair_at(float(scaling.get("slow", 1.0)))), rotary - 1)
+        ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+        freq = freq * (1.0 - ramp) + freq / f * ramp
+        mscale = float(scaling.get("mscale", 0.1 * math.log(f) + 1.0 if f > 1.0 else 1.0))
+    return freq.to(device) if device is not None else freq, mscale
+
+
+def sha_rope(x, positions, inv_freq, out=None, interleaved=False, mscale=1.0, stream=None):
+    """Rotary positions: x [T, H, d] (any strides, d contiguous; float16 or bfloat16),
+    positions int32 [T], inv_freq float64 [rotary/2] (rope_frequencies), all on one
+    device.  out (default: a new contiguous tensor) may be x itself.  Rotating by
+    -positions is the inverse up to mscale^2, and the gradient."""
+    _check_heads_view("x", x)
+    dev = x.device
+    T, H, d = x.shape
+    _check_vector("positions", positions, T, torch.int32, dev)
+    _check_inv_freq(inv_freq, dev)
+    if out is None:
+        out = torch.empty((T, H, d), dtype=x.dtype, device=dev)
+    else:
+        _check_heads_view("out", out, x)
+        if out.shape != x.shape:
+            raise ValueError("out must have x's shape")
+    _on_device(dev, _lib.sha_rope, x.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), T, H, d,
+               2 * inv_freq.shape[0], 1 if interleaved else 0, mscale,
+               _i64x2(x.stride(0), x.stride(1)), out.data_ptr(),
+               _i64x2(out.stride(0), out.stride(1)), _dtype_code(x.dtype), stream=stream)
+    return out
+
+
+def sha_append_paged(k, v, k_pages, v_pages, block_table, positions, rows=None, inv_freq=None,
+                     interleaved=False, mscale=1.0, q=None, q_out=None, stream=None):
+    """Append the tokens' keys and values to a paged cache (that of sha_decode_paged)
+    and rotate their queries, in one launch.  k, v [T, H_kv, d] views with d
+    contiguous; positions int32 [T]: each token's place in its row (-1: no token);
+    rows int32 [T]: its row of block_table (default: token t is row t's).  With
+    inv_freq (float64 [rotary/2]) keys turn by their position on the way, and q
+    [T, H_q, d] turns into q_out (default: a new tensor; may be q itself).  Returns
+    q_out (None without q)."""
+    _check_heads_view("k", k)
+    _check_heads_view("v", v, k)
+    T, H_kv, d = k.shape
+    if v.shape != k.shape:
+        raise ValueError("v must have k's shape")
+    dev = k.device
+    if k_pages.dim() != 4 or k_pages.shape[1] != H_kv or k_pages.shape[3] != d \
+            or v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must both be [num_pages, H_kv, page_size, d]")
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if t.dtype != k.dtype or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {k.dtype} tensor on {dev}")
+    if block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.device != dev \
+            or not block_table.is_contiguous():
+        raise ValueError(f"block_table must be a contiguous int32 [B, max_pages] tensor on {dev}")
+    _check_vector("positions", positions, T, torch.int32, dev)
+    if rows is not None:
+        _check_vector("rows", rows, T, torch.int32, dev)
+    rotary, freq = 0, None
+    if inv_freq is not None:
+        _check_inv_freq(inv_freq, dev)
+        rotary, freq = 2 * inv_freq.shape[0], inv_freq.data_ptr()
+    H_q, qp, qs, op, os_ = 0, None, None, None, None
+    if q is not None:
+        if inv_freq is None:
+            raise ValueError("q needs inv_freq: without a rotation there is nothing to do to it")
+        _check_heads_view("q", q, k)
+        if q.shape[0] != T or q.shape[2] != d:
+            raise ValueError("q must be [T, H_q, d]")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        else:
+            _check_heads_view("q_out", q_out, k)
+            if q_out.shape != q.shape:
+                raise ValueError("q_out must have q's shape")
+        H_q, qp, op = q.shape[1], q.data_ptr(), q_out.data_ptr()
+        qs, os_ = _i64x2(q.stride(0), q.stride(1)), _i64x2(q_out.stride(0), q_out.stride(1))
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _on_device(dev, _lib.sha_append_paged, k.data_ptr(), v.data_ptr(),
+               _i64x2(k.stride(0), k.stride(1)), _i64x2(v.stride(0), v.stride(1)), T, H_kv, d,
+               k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+               None if rows is None else rows.data_ptr(), positions.data_ptr(),
+               block_table.shape[0], k_pages.shape[0], k_pages.shape[2], block_table.shape[1], freq,
+               rotary, 1 if interleaved else 0, mscale, qp, qs, H_q, op, os_,
+               _dtype_code(k.dtype), stream=stream)
+    return q_out
+
+
 def sha_get_device_status(stream=None, device=None):
     """Synchronise ``stream`` and read-and-clear the device's sticky flags; returns a
     status code (SHA_OK, SHA_ERR_BAD_INDEX or SHA_ERR_TIMEOUT)."""
@@ -537,4 +729,5 @@ __all__ = [
     "sha_selective_mlp", "sha_selective_mlp_workspace_size", "sha_selective_mlp_plan",
     "sha_copy_bandwidth_probe", "decode",
     "alloc_workspace", "ShaError", "LIBRARY_PATH", "sha_decode_noalloc",
+    "rope_frequencies", "sha_rope", "sha_append_paged",
 ]

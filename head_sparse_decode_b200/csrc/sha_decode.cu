@@ -877,6 +877,11 @@ __global__ void copy_probe_kernel(uint4 *__restrict__ dst, const uint4 *__restri
 
 }  // namespace
 
+// The other translation units of the library: their launch errors, read by
+// sha_last_cuda_error(), and their sticky device flags, taken and cleared.
+sha_status_t sha_launch_failed(cudaError_t e) { return launch_error(e); }
+unsigned sha_rope_take_status();   // sha_rope.cu
+
 extern "C" {
 
 sha_status_t sha_decode(const void *q, const void *k, const void *v,
@@ -1098,6 +1103,7 @@ sha_status_t sha_get_device_status(void *stream)
     e = cudaMemcpyToSymbol(sha::g_sha_status, &zero, sizeof zero);
     if (e != cudaSuccess) return launch_error(e);
     flags |= sha_mlp_take_status();
+    flags |= sha_rope_take_status();
     if (flags & sha::kStatusTimeout) {
         // an abandoned merge can leave arrival counters raised: clear the
         // library workspace's, in order on `stream`

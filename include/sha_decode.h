@@ -391,6 +391,74 @@ sha_status_t sha_selective_mlp(const void *x, const void *W1t, const void *W2t,
                                size_t workspace_bytes, void *stream);
 
 /*
+ * ---- Positions and the paged cache ------------------------------------------
+ * The steps of a serving loop on either side of the decode: rotary positions,
+ * appending the new tokens' keys and values to the paged cache that
+ * sha_decode_paged reads, and decoding a batch whose rows share a prefix.  The
+ * pages evaluate models that use rotary positions (LLaMA-2-7B, LLaMA-3.1-70B;
+ * papernotes.org summary, ablation table) but describe neither step.
+ *
+ * sha_rope -- rotary positions: the first `rotary` elements of each head of each
+ * token turn, in pairs, by positions[t] * inv_freq[i]; the rest are copied.
+ *     out1 = mscale * (x1 cos a - x2 sin a),  out2 = mscale * (x2 cos a + x1 sin a)
+ *   x, out      : [T, H, d] views, d contiguous; element (t, h, e) of x is at
+ *                 x + t*x_strides[0] + h*x_strides[1] + e (strides in elements,
+ *                 host arrays of 2 int64, each >= 0 -- for out >= d -- and a
+ *                 multiple of 8; the stride of a dimension of size 1 is not
+ *                 used).  out may be x itself (the same pointer and strides);
+ *                 otherwise the two must not overlap.
+ *   positions   : device, int32 [T].  Negative positions turn backwards:
+ *                 rotating by -positions undoes a rotation (up to mscale^2), and
+ *                 is the gradient of a rotation by positions.
+ *   inv_freq    : device, fp64 [rotary/2], radians per position.  Long-context
+ *                 scaling of the frequencies is in this table, its factor on
+ *                 the result in mscale (finite; 1 without one).
+ *   d           : a multiple of 8, at most 512 (SHA_ERR_UNSUPPORTED otherwise)
+ *   rotary      : even, 2 <= rotary <= d
+ *   interleaved : 0: pair i is elements (i, i + rotary/2); 1: (2i, 2i + 1)
+ *   x, out 16-byte aligned, inv_freq 8-byte, positions 4-byte
+ *   (SHA_ERR_MISALIGNED otherwise).
+ * The angle is formed and reduced in fp64, the rest is fp32, the result is
+ * rounded once.  Needs no workspace.
+ */
+sha_status_t sha_rope(const void *x, const int32_t *positions, const double *inv_freq, int T,
+                      int H, int d, int rotary, int interleaved, float mscale,
+                      const int64_t x_strides[2], void *out, const int64_t out_strides[2],
+                      sha_dtype_t dtype, void *stream);
+
+/*
+ * sha_append_paged -- write the keys and values of T new tokens into a paged
+ * cache, the keys rotated on the way, and rotate the tokens' queries in the same
+ * launch.  Token t belongs to row r = rows[t] (t itself if rows is NULL, and then
+ * T <= B) and lands at cache position p = positions[t] of it: page
+ * block_table[r, p / page_size], key p % page_size, for every KV head.  p is the
+ * rotation's position too.
+ *   k, v        : [T, H_kv, d] views as in sha_rope (e.g. slices of a fused
+ *                 projection's rows)
+ *   k_pages, v_pages, block_table, num_pages, page_size, max_pages: the cache of
+ *                 sha_decode_paged (block_table int32 [B, max_pages]); any
+ *                 page_size >= 1
+ *   positions   : device, int32 [T].  -1 marks no token (the padding of a
+ *                 captured batch): nothing is written for it, q included.
+ *   inv_freq, rotary, interleaved, mscale: as for sha_rope; rotary = 0 appends
+ *                 without rotation (then H_q = 0 and inv_freq may be NULL)
+ *   q, q_out    : [T, H_q, d] views; q_out may be q itself.  H_q = 0: no queries.
+ * A row outside [0, B), a position outside [0, max_pages * page_size) or a page
+ * id outside [0, num_pages) is bad input: the SHA_ERR_BAD_INDEX flag is raised
+ * and nothing is written for that token.  Two tokens of one call must not name
+ * the same cache slot (its contents are then unspecified).  k, v, q and q_out
+ * must not overlap the pools.  Needs no workspace.
+ */
+sha_status_t sha_append_paged(const void *k, const void *v, const int64_t k_strides[2],
+                              const int64_t v_strides[2], int T, int H_kv, int d, void *k_pages,
+                              void *v_pages, const int32_t *block_table, const int32_t *rows,
+                              const int32_t *positions, int B, int num_pages, int page_size,
+                              int max_pages, const double *inv_freq, int rotary, int interleaved,
+                              float mscale, const void *q, const int64_t q_strides[2], int H_q,
+                              void *q_out, const int64_t q_out_strides[2], sha_dtype_t dtype,
+                              void *stream);
+
+/*
  * sha_get_device_status -- synchronises `stream`, then reads and clears the
  * current device's sticky flags: SHA_ERR_BAD_INDEX if any call since the last
  * read met an out-of-range head id, SHA_ERR_TIMEOUT if a pipeline wait gave
