@@ -47,6 +47,7 @@ SHA_BF16 = 1
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
+_f = ctypes.c_float
 _DECODE_ARGS = [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, ctypes.c_float, _vp, _vp]
 _lib.sha_decode.argtypes = _DECODE_ARGS
 _lib.sha_decode.restype = _i
@@ -255,6 +256,77 @@ def sha_decode_strided(q, k, v, batch_head_index, scale, out, seqlens=None, stre
             None if seqlens is None else seqlens.data_ptr(), B, H_q, H_kv,
             N_kv, d, batch_head_index.shape[1], _default_scale(scale, d), out.data_ptr(), ks, vs,
             _dtype_code(k.dtype), _stream_handle(stream, k.device)))
+    return out
+
+
+_lib.sha_decode_prefix.argtypes = [_vp] * 7 + [_i] * 9 + [_f, _vp, _i, _vp, ctypes.c_size_t, _vp]
+_lib.sha_decode_prefix.restype = _i
+_lib.sha_decode_prefix_workspace_size.argtypes = [_i] * 5
+_lib.sha_decode_prefix_workspace_size.restype = ctypes.c_size_t
+
+
+def sha_decode_prefix_workspace_size(B, H_q, H_kv, d, top_k, device=None):
+    """Workspace bytes sha_decode_prefix needs for these sizes on ``device``."""
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        return int(_lib.sha_decode_prefix_workspace_size(B, H_q, H_kv, d, top_k))
+
+
+def sha_decode_prefix(q, k_pages, v_pages, batch_head_index, seqlens, block_table, prefix_len,
+                      prefix_table, scale, out, workspace=None, stream=None):
+    """sha_decode_paged for rows that all begin with the same ``prefix_len`` keys: the
+    attention over the shared keys, which lie in the pages of prefix_table (int32
+    [ceil(prefix_len / page_size)]), is computed once per KV head for all the rows that
+    select it.  seqlens (int32 [B], each >= prefix_len) are whole lengths; block_table
+    rows cover the whole sequences, their entries for the prefix unread.  workspace
+    (default: a new tensor) is uint8, at least sha_decode_prefix_workspace_size bytes;
+    calls that share it must not overlap."""
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must both be [num_pages, H_kv, page_size, d]")
+    num_pages, H_kv, page_size, d = k_pages.shape
+    dev, dtype = k_pages.device, k_pages.dtype
+    if not k_pages.is_cuda:
+        raise ValueError("k_pages must be a CUDA tensor")
+    if q.dim() == 4 and q.shape[2] != 1:
+        raise ValueError("decode takes one query token: q must be [B, H_q, 1, d]")
+    if q.dim() not in (3, 4) or q.shape[-1] != d:
+        raise ValueError("q must be [B, H_q, d] or [B, H_q, 1, d]")
+    B, H_q = q.shape[0], q.shape[1]
+    if out.numel() != B * H_q * d:
+        raise ValueError("out must hold [B, H_q, d] elements")
+    if batch_head_index.dim() != 2 or batch_head_index.shape[0] != B:
+        raise ValueError("batch_head_index must be [B, top_k]")
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, max_pages]")
+    prefix_len = int(prefix_len)
+    if prefix_len < 1:
+        raise ValueError("prefix_len must be at least 1 (without a prefix: sha_decode_paged)")
+    if prefix_table.dim() != 1 or prefix_table.shape[0] * page_size < prefix_len:
+        raise ValueError("prefix_table must hold ceil(prefix_len / page_size) page ids")
+    if seqlens.shape != (B,):
+        raise ValueError("seqlens must be [B]")
+    for name, t, dt in (("q", q, dtype), ("k_pages", k_pages, dtype), ("v_pages", v_pages, dtype),
+                        ("out", out, dtype), ("batch_head_index", batch_head_index, torch.int32),
+                        ("seqlens", seqlens, torch.int32), ("block_table", block_table, torch.int32),
+                        ("prefix_table", prefix_table, torch.int32)):
+        if t.dtype != dt or not t.is_contiguous() or t.device != dev:
+            raise ValueError(f"{name} must be a contiguous {dt} tensor on {dev}")
+    top_k = batch_head_index.shape[1]
+    code = _dtype_code(dtype)
+    handle = _stream_handle(stream, dev)
+    with torch.cuda.device(dev):
+        if workspace is None:
+            nbytes = _lib.sha_decode_prefix_workspace_size(B, H_q, H_kv, d, top_k)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            if handle != torch.cuda.current_stream(dev).cuda_stream:
+                workspace.record_stream(torch.cuda.ExternalStream(handle, device=dev))
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+        _check(_lib.sha_decode_prefix(
+            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), batch_head_index.data_ptr(),
+            seqlens.data_ptr(), block_table.data_ptr(), prefix_table.data_ptr(), prefix_len, B, H_q,
+            H_kv, num_pages, page_size, block_table.shape[1], d, top_k, _default_scale(scale, d),
+            out.data_ptr(), code, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), handle))
     return out
 
 
@@ -512,7 +584,6 @@ def sha_selective_mlp(x, W1t, W2t, S, n_S, y=None, activation="relu", workspace=
 
 
 _i64x2 = ctypes.c_int64 * 2
-_f = ctypes.c_float
 _lib.sha_rope.argtypes = [_vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _vp, _vp, _vp, _i, _vp]
 _lib.sha_rope.restype = _i
 _lib.sha_append_paged.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _i, _i,
@@ -729,5 +800,6 @@ __all__ = [
     "sha_selective_mlp", "sha_selective_mlp_workspace_size", "sha_selective_mlp_plan",
     "sha_copy_bandwidth_probe", "decode",
     "alloc_workspace", "ShaError", "LIBRARY_PATH", "sha_decode_noalloc",
-    "rope_frequencies", "sha_rope", "sha_append_paged",
+    "rope_frequencies", "sha_rope", "sha_append_paged", "sha_decode_prefix",
+    "sha_decode_prefix_workspace_size",
 ]

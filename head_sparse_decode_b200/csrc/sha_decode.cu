@@ -14,6 +14,7 @@
 #include "sha_device.cuh"
 #include "sha_gqa_kernel.cuh"
 #include "sha_mha_kernel.cuh"
+#include "sha_prefix_kernel.cuh"
 #include "sha_schedule.cuh"
 #include "sha_select_kernel.cuh"
 
@@ -549,7 +550,7 @@ sha_status_t launch_gqa(const sha::DecodeParams &prm, sha_dtype_t dtype, int dev
         return SHA_OK;
     }
     // a padded cache: [B*H_kv][N_kv][d]; a page pool: [num_pages*H_kv][page_size][d]
-    const bool paged = kLayout == sha::kLayoutPaged;
+    const bool paged = sha::layout_paged(kLayout);
     const long long planes = paged ? (long long)prm.num_pages * prm.H_kv : (long long)prm.B * prm.H_kv;
     const int rows = paged ? prm.page_size : prm.N_kv;
     const int box_rows = paged && prm.page_size < C::kTile ? prm.page_size : C::kTile;
@@ -833,6 +834,9 @@ sha_status_t decode_impl(const void *q, const void *k, const void *v, const int3
     prm.batch_dim = 2;
     prm.tokens = lay.tokens;
     prm.n_sel = lay.n_sel;
+    prm.min_len = 1;
+    prm.key0 = 0;
+    prm.prefix = {};
     if (lay.strided) {
         StridedMaps kv;
         int vt, vh, vb;
@@ -855,6 +859,81 @@ sha_status_t decode_impl(const void *q, const void *k, const void *v, const int3
     if (lay.block_table) return launch_decode<sha::kLayoutPaged>(prm, dtype, d, fma, look, dev, s);
     if (seqlens) return launch_decode<sha::kLayoutVarlen>(prm, dtype, d, fma, look, dev, s);
     return launch_decode<sha::kLayoutFixed>(prm, dtype, d, fma, look, dev, s);
+}
+
+// Workspace of a shared-prefix call: the suffix pass's arrival counters, the
+// units' references to their prefix parts, the suffix pass's partial states and
+// the prefix pass's.
+struct PrefixPlan {
+    long long units;
+    int row_tiles_max;           // row tiles the selection can need, at most
+    int suffix_slot_floats, prefix_slot_floats;
+    size_t ref_at, suffix_at, prefix_at, bytes;
+};
+
+template <int D>
+PrefixPlan make_prefix_plan(int B, int H_q, int H_kv, int top_k, int num_sms)
+{
+    using C = sha::PrefixConfig<D>;
+    PrefixPlan pl;
+    const int G = H_q / H_kv;
+    const int per_tile = C::kRows / G;
+    pl.units = (long long)B * top_k;
+    // each head's last row tile may be ragged; the others are full
+    pl.row_tiles_max = (int)(pl.units / per_tile + (pl.units < H_kv ? pl.units : H_kv));
+    pl.suffix_slot_floats = (G * (D + 2) + 31) / 32 * 32;
+    pl.prefix_slot_floats = C::kRows * (D + 2);
+    auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+    pl.ref_at = sha::kCounterBytes;
+    pl.suffix_at = pl.ref_at + up((size_t)pl.units * sizeof(int4));
+    pl.prefix_at = pl.suffix_at + up((size_t)2 * num_sms * pl.suffix_slot_floats * sizeof(float));
+    pl.bytes = pl.prefix_at +
+               up((size_t)(pl.row_tiles_max + num_sms) * pl.prefix_slot_floats * sizeof(float));
+    return pl;
+}
+
+PrefixPlan make_prefix_plan(int B, int H_q, int H_kv, int d, int top_k, int num_sms)
+{
+    return d == 128 ? make_prefix_plan<128>(B, H_q, H_kv, top_k, num_sms)
+                    : make_prefix_plan<64>(B, H_q, H_kv, top_k, num_sms);
+}
+
+// Units of one call; its indexes and slots stay within 32 bits.
+constexpr long long kMaxPrefixUnits = 1 << 24;
+
+sha_status_t check_prefix_shape(int B, int H_q, int H_kv, int d, int top_k)
+{
+    sha_status_t st = check_shape(B, H_q, H_kv, 1, d, top_k, 1.0f);
+    if (st != SHA_OK) return st;
+    if (H_kv > sha::kPrefixMaxHeads || (long long)B * top_k > kMaxPrefixUnits)
+        return SHA_ERR_UNSUPPORTED;
+    return SHA_OK;
+}
+
+template <typename T, int D>
+sha_status_t launch_prefix(const sha::PrefixParams &prm, const void *k, const void *v,
+                           const sha::DecodeParams &suffix, sha_dtype_t dtype, int num_sms,
+                           int dev, cudaStream_t stream)
+{
+    using C = sha::PrefixConfig<D>;
+    auto kernel = sha::sha_prefix_kernel<T, D>;
+    static std::atomic<bool> configured[kMaxDevices];
+    if (!configured[dev].load(std::memory_order_acquire)) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             C::kSmemBytes);
+        if (e != cudaSuccess) return launch_error(e);
+        configured[dev].store(true, std::memory_order_release);
+    }
+    const int box_rows = prm.page_size < C::kTile ? prm.page_size : C::kTile;
+    const long long planes = (long long)prm.num_pages * prm.H_kv;
+    CUtensorMap tm_k, tm_v;
+    sha_status_t st = kv_tensor_map(&tm_k, k, dtype, D, prm.page_size, planes, box_rows);
+    if (st == SHA_OK) st = kv_tensor_map(&tm_v, v, dtype, D, prm.page_size, planes, box_rows);
+    if (st != SHA_OK) return st;
+    cudaError_t e = launch_kernel(kernel, num_sms, C::kThreads, C::kSmemBytes, stream, prm, tm_k,
+                                  tm_v);
+    if (e != cudaSuccess) return launch_error(e);
+    return launch_gqa<T, D, sha::kLayoutSuffix, false>(suffix, dtype, dev, stream, nullptr);
 }
 
 __global__ void copy_probe_kernel(uint4 *__restrict__ dst, const uint4 *__restrict__ src,
@@ -978,6 +1057,105 @@ sha_status_t sha_decode_tokens(const void *q, const void *k, const void *v,
     lay.n_sel = n_sel;
     return decode_impl(q, k, v, batch_head_index, B, H_q, H_kv, N_kv, d, top_k, scale, out,
                        dtype, nullptr, 0, 0, stream, true, lay);
+}
+
+size_t sha_decode_prefix_workspace_size(int B, int H_q, int H_kv, int d, int top_k)
+{
+    if (check_prefix_shape(B, H_q, H_kv, d, top_k) != SHA_OK || B == 0 || top_k == 0) return 0;
+    int dev;
+    DeviceInfo *info;
+    if (current_device(&dev, &info) != SHA_OK) return 0;
+    return make_prefix_plan(B, H_q, H_kv, d, top_k, info->num_sms).bytes;
+}
+
+sha_status_t sha_decode_prefix(const void *q, const void *k_pages, const void *v_pages,
+                               const int32_t *batch_head_index, const int32_t *seqlens,
+                               const int32_t *block_table, const int32_t *prefix_table,
+                               int prefix_len, int B, int H_q, int H_kv, int num_pages,
+                               int page_size, int max_pages, int d, int top_k, float scale,
+                               void *out, sha_dtype_t dtype, void *workspace,
+                               size_t workspace_bytes, void *stream)
+{
+    if (dtype != SHA_FP16 && dtype != SHA_BF16) return SHA_ERR_UNSUPPORTED;
+    if (num_pages < 1 || page_size < 1 || max_pages < 1 || prefix_len < 1) return SHA_ERR_INVALID_ARG;
+    if ((long long)max_pages * page_size > (1 << 30) || prefix_len > max_pages * page_size)
+        return SHA_ERR_INVALID_ARG;
+    if (!std::isfinite(scale)) return SHA_ERR_INVALID_ARG;
+    sha_status_t st = check_prefix_shape(B, H_q, H_kv, d, top_k);
+    if (st != SHA_OK) return st;
+    if (!boxable_pages(page_size) || (long long)num_pages * H_kv > (1ll << 31) - 1)
+        return SHA_ERR_UNSUPPORTED;
+    if (B == 0 || top_k == 0) return SHA_OK;
+    if (!q || !k_pages || !v_pages || !batch_head_index || !seqlens || !block_table ||
+        !prefix_table || !out)
+        return SHA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16) ||
+        !aligned(batch_head_index, 4) || !aligned(seqlens, 4) || !aligned(block_table, 4) ||
+        !aligned(prefix_table, 4) || !aligned(workspace, 256))
+        return SHA_ERR_MISALIGNED;
+
+    int dev;
+    DeviceInfo *info;
+    st = current_device(&dev, &info);
+    if (st != SHA_OK) return st;
+    const PrefixPlan pl = make_prefix_plan(B, H_q, H_kv, d, top_k, info->num_sms);
+    if (!workspace || workspace_bytes < pl.bytes) return SHA_ERR_WORKSPACE;
+    char *ws = static_cast<char *>(workspace);
+
+    sha::PrefixParams prm;
+    prm.q = q;
+    prm.idx = batch_head_index;
+    prm.table = prefix_table;
+    prm.B = B;
+    prm.H_q = H_q;
+    prm.H_kv = H_kv;
+    prm.top_k = top_k;
+    prm.keys = prefix_len;
+    prm.page_size = page_size;
+    prm.num_pages = num_pages;
+    prm.scale_log2 = scale * 1.4426950408889634f;
+    prm.parts.ref = reinterpret_cast<int4 *>(ws + pl.ref_at);
+    prm.parts.slots = reinterpret_cast<float *>(ws + pl.prefix_at);
+    prm.parts.slot_floats = pl.prefix_slot_floats;
+    prm.parts.slot_rows = pl.prefix_slot_floats / (d + 2);
+    prm.counters = reinterpret_cast<int *>(ws);
+    prm.num_counters = info->num_sms;
+
+    sha::DecodeParams suf = {};
+    suf.q = q;
+    suf.k = k_pages;
+    suf.v = v_pages;
+    suf.idx = batch_head_index;
+    suf.out = out;
+    suf.B = B;
+    suf.H_q = H_q;
+    suf.H_kv = H_kv;
+    suf.N_kv = max_pages * page_size;
+    suf.top_k = top_k;
+    suf.scale_log2 = prm.scale_log2;
+    suf.sched.num_ctas = info->num_sms;      // the device plans an even cut of these
+    suf.slots = reinterpret_cast<float *>(ws + pl.suffix_at);
+    suf.slot_floats = pl.suffix_slot_floats;
+    suf.counters = prm.counters;
+    suf.seqlens = seqlens;
+    suf.block_table = block_table;
+    suf.page_size = page_size;
+    suf.max_pages = max_pages;
+    suf.num_pages = num_pages;
+    suf.min_len = prefix_len;
+    // the last box boundary at or before the prefix's end
+    const int box = page_size < sha::GqaConfig<128>::kTile ? page_size : sha::GqaConfig<128>::kTile;
+    suf.key0 = prefix_len / box * box;
+    suf.prefix = prm.parts;
+
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int sms = info->num_sms;
+    if (dtype == SHA_FP16)
+        return d == 128 ? launch_prefix<__half, 128>(prm, k_pages, v_pages, suf, dtype, sms, dev, s)
+                        : launch_prefix<__half, 64>(prm, k_pages, v_pages, suf, dtype, sms, dev, s);
+    return d == 128
+               ? launch_prefix<__nv_bfloat16, 128>(prm, k_pages, v_pages, suf, dtype, sms, dev, s)
+               : launch_prefix<__nv_bfloat16, 64>(prm, k_pages, v_pages, suf, dtype, sms, dev, s);
 }
 
 size_t sha_decode_workspace_size(int B, int H_q, int H_kv, int N_kv, int d, int top_k,

@@ -148,6 +148,60 @@ __device__ __forceinline__ uint32_t swizzled(uint32_t tile, int key, int chunk)
     return tile + box * C::kBoxBytes + key * 128 + ((c ^ (key & 7)) << 4);
 }
 
+// Four neighbouring elements of an output row being put together from partial
+// states (O, m, l) by the log-sum-exp rule, in the order they are folded in.
+template <typename T>
+struct FoldedRow {
+    float4 O;
+    float M, L;
+
+    __device__ __forceinline__ void start(float m, float l)
+    {
+        O = make_float4(0.f, 0.f, 0.f, 0.f);
+        M = m;
+        L = l;
+    }
+    // a term already in terms of M (a warp's share of this block's state)
+    __device__ __forceinline__ void add(float w, float2 a, float2 b)
+    {
+        O.x = fmaf(w, a.x, O.x);
+        O.y = fmaf(w, a.y, O.y);
+        O.z = fmaf(w, b.x, O.z);
+        O.w = fmaf(w, b.y, O.w);
+    }
+    __device__ __forceinline__ void fold(float m, float l, float4 x)
+    {
+        const float top = fmaxf(M, m);
+        const float ref = top == -INFINITY ? 0.f : top;
+        const float a = exp2f(M - ref), b = exp2f(m - ref);
+        O.x = fmaf(b, x.x, a * O.x);
+        O.y = fmaf(b, x.y, a * O.y);
+        O.z = fmaf(b, x.z, a * O.z);
+        O.w = fmaf(b, x.w, a * O.w);
+        L = fmaf(b, l, a * L);
+        M = top;
+    }
+    __device__ __forceinline__ void fold_prefix(const PrefixParts &p, const int4 &ref, int row,
+                                                int c, int D)
+    {
+        const float *slot = p.slots + (size_t)ref.x * p.slot_floats;
+        const int r = ref.z + row;
+#pragma unroll 4
+        for (int i = 0; i < ref.y; ++i, slot += p.slot_floats) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(
+                slot + (size_t)p.slot_rows * D + 2 * r));
+            const float4 x =
+                __ldcg(reinterpret_cast<const float4 *>(slot + (size_t)r * D + c));
+            fold(ml.x, ml.y, x);
+        }
+    }
+    __device__ __forceinline__ void store(T *out)
+    {
+        *reinterpret_cast<uint2 *>(out) =
+            make_uint2(pack2<T>(O.x / L, O.y / L), pack2<T>(O.z / L, O.w / L));
+    }
+};
+
 template <typename T, int D, int kLayout, bool kLook>
 __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == kLayoutTokens), 1)
     sha_gqa_decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm_k,
@@ -155,6 +209,7 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
 {
     constexpr bool kVarlen = layout_varlen(kLayout);
     constexpr bool kCluster = kLayout == kLayoutCluster;
+    constexpr bool kSuffix = kLayout == kLayoutSuffix;
     using Walk = typename std::conditional<
         kVarlen, VarlenWalk,
         typename std::conditional<kCluster, ClusterWalk, UniformWalk>::type>::type;
@@ -208,18 +263,23 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v))
                      : "memory");
     }
-    // inputs, workspace and the output may come from the previous kernel
-    pdl_wait();
+    // inputs, workspace and the output may come from the previous kernel.  The
+    // kernel before a suffix pass is the prefix pass of the same call: it started
+    // after everything before it had finished, and writes nothing that is read
+    // before the first unit is put together, where it is waited for.
+    if constexpr (!kSuffix) pdl_wait();
     pdl_launch_dependents();
     if constexpr (kCluster) cluster_wait();
 
     Schedule S = p.sched;
     Walk walk;
     if constexpr (kVarlen) {
-        if (!varlen_plan<C::threads(kLook)>(p.seqlens, p.B, p.top_k, p.N_kv, C::kTile, gridDim.x,
+        if (!varlen_plan<C::threads(kLook)>(p.seqlens, p.B, p.top_k, p.keys(), C::kTile, gridDim.x,
                                       reinterpret_cast<long long *>(smem + C::kPlanOffset), S,
-                                      walk))
+                                      walk)) {
+            if constexpr (kSuffix) pdl_wait();
             return;
+        }
     } else if constexpr (kCluster) {
         walk.start(S, (long long)p.B * p.top_k, p.N_kv);
     } else {
@@ -249,7 +309,7 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
     if (gw >= 0) {
         // A paged cache needs several page ids per tile: the whole warp gathers
         // them (one page box per lane).  Otherwise one lane drives the pipeline.
-        constexpr bool kWarpProducer = kLayout == kLayoutPaged || kLayout == kLayoutTokens;
+        constexpr bool kWarpProducer = layout_paged(kLayout) || kLayout == kLayoutTokens;
         if (!kWarpProducer && lane != 0) {
             if constexpr (kCluster) cluster_sync_unaligned();
             return;
@@ -299,7 +359,7 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
                 }
                 if constexpr (kWarpProducer) go = __shfl_sync(0xffffffffu, go, 0);
                 if (!go) { ok = false; break; }
-                if constexpr (kLayout == kLayoutPaged) {
+                if constexpr (layout_paged(kLayout)) {
                     // boxes of min(page_size, tile) keys, each inside one page,
                     // landing at 1 KiB-aligned rows of the swizzled tile
                     const int n0 = j * C::kTile;
@@ -312,7 +372,7 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
                     __syncwarp();
                     const int32_t *bt = p.block_table + (size_t)b * p.max_pages;
                     for (int c = lane; c < chunks; c += 32) {
-                        const int key = n0 + c * box_rows;
+                        const int key = (kSuffix ? p.key0 : 0) + n0 + c * box_rows;
                         const int pi = key / p.page_size, off = key - pi * p.page_size;
                         int page = bt[pi];
                         if ((unsigned)page >= (unsigned)p.num_pages) {
@@ -461,6 +521,8 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
 
     Walk wk = walk;
     Seg seg;
+    bool waited = false;   // suffix: the prefix pass has finished
+    (void)waited;
     int n_done = 0;   // clustered cut: units this block has finished (its buffers' parity)
     for (bool first_seg = true; wk.next(seg); first_seg = false) {
         const long long u = seg.unit;
@@ -505,16 +567,18 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
                 const uint32_t kt = k_base + stage * C::kTileBytes;
                 const uint32_t vt = v_base + stage * C::kTileBytes;
                 const int rows = min(C::kTile, seg.n_keys - j * C::kTile);
+                // a suffix's first tile begins with the prefix's last keys
+                const int lo = kSuffix && j == 0 ? p.min_len - p.key0 : 0;
                 if constexpr (kVarlen) {
                     // keys past this row's length but inside the cache hold stale
                     // values: zero this warp's V rows there (0 * NaN would poison P V)
-                    if (rows < C::kTile) {
+                    if (rows < C::kTile || lo > 0) {
                         unsigned char *vtile = v_ring + stage * C::kTileBytes;
                         for (int i = lane; i < C::kSlices * 16 * C::kBoxes * 8; i += 32) {
                             const int chunk = i & 7, bx = (i >> 3) % C::kBoxes;
                             const int rr = (i >> 3) / C::kBoxes;      // 0 .. kSlices*16-1
                             const int key = (rr >> 4) * 64 + warp * C::kKeysPerWarp + (rr & 15);
-                            if (key >= rows)
+                            if (key >= rows || key < lo)
                                 *reinterpret_cast<uint4 *>(vtile + bx * C::kBoxBytes + key * 128 +
                                                            chunk * 16) = make_uint4(0, 0, 0, 0);
                         }
@@ -550,7 +614,9 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
                         for (int e = 0; e < 4; ++e) {
                             const int key = sl * 64 + warp * C::kKeysPerWarp + nt * 8 + qd * 2 +
                                             (e & 1);
-                            s[sl][nt][e] = key < rows ? s[sl][nt][e] * p.scale_log2 : -INFINITY;
+                            s[sl][nt][e] = key < rows && key >= lo
+                                               ? s[sl][nt][e] * p.scale_log2
+                                               : -INFINITY;
                             mt[e >> 1] = fmaxf(mt[e >> 1], s[sl][nt][e]);
                         }
                 float alpha[2], ref[2];
@@ -664,6 +730,14 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
                     : p.slots ? p.slots + (size_t)(2 * blockIdx.x + (first_seg ? 0 : 1)) *
                                               p.slot_floats
                               : nullptr;
+        // the unit's parts over a shared prefix: the kernel that computed them has
+        // run beside this one's first streaming, and is waited for here
+        int4 pref = make_int4(0, 0, 0, 0);
+        if constexpr (kSuffix) {
+            if (!waited) pdl_wait();
+            waited = true;
+            pref = __ldcg(p.prefix.ref + u);
+        }
         // under the clustered cut, a unit that is not whole here is shared by
         // the cluster's blocks
         bool shared = false;
@@ -696,8 +770,25 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
                                cr[C::kConsumerWarps + 1], &cbar[buf]);
             }
         } else if (!aborted) {
+            if (kSuffix && seg.whole) {
+                // four elements of a row per thread, the prefix's parts folded in
+                for (int e = 4 * tid; e < G * D; e += 4 * C::kConsumers) {
+                    const int row = e / D, c = e - row * D;
+                    const float *cr = cw + row * C::kCombineFloats;
+                    FoldedRow<T> f;
+                    f.start(cr[C::kConsumerWarps], cr[C::kConsumerWarps + 1]);
+#pragma unroll
+                    for (int w = 0; w < C::kConsumerWarps; ++w) {
+                        const float *st = wstate + w * C::kStateFloats + row * (D + 2) + c;
+                        f.add(cr[w], *reinterpret_cast<const float2 *>(st),
+                              *reinterpret_cast<const float2 *>(st + 2));
+                    }
+                    f.fold_prefix(p.prefix, pref, row, c, D);
+                    f.store(out_g + e);
+                }
+            }
             // two neighbouring elements of a row per thread (D is even)
-            for (int e = 2 * tid; e < G * D; e += 2 * C::kConsumers) {
+            for (int e = kSuffix && seg.whole ? G * D : 2 * tid; e < G * D; e += 2 * C::kConsumers) {
                 const int row = e / D, c = e - row * D;
                 const float *cr = cw + row * C::kCombineFloats;
                 float2 O = make_float2(0.f, 0.f);
@@ -766,7 +857,24 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
                 flags[1] = merge;
             }
             named_barrier(1, C::kConsumers);
-            if (flags[1]) {
+            if (kSuffix && flags[1]) {
+                __threadfence();
+                const int parts = last - first + 1;
+                for (int e = 4 * tid; e < G * D; e += 4 * C::kConsumers) {
+                    const int row = e / D, c = e - row * D;
+                    FoldedRow<T> f;
+                    f.start(-INFINITY, 0.f);
+                    for (int i = 0; i < parts; ++i) {
+                        const float *part =
+                            p.slots + (size_t)merge_slot(first, first_slot, i) * p.slot_floats;
+                        f.fold(__ldcg(part + G * D + row), __ldcg(part + G * D + G + row),
+                               __ldcg(reinterpret_cast<const float4 *>(part + e)));
+                    }
+                    f.fold_prefix(p.prefix, pref, row, c, D);
+                    f.store(out_g + e);
+                }
+                if (tid == 0) p.counters[first] = 0;
+            } else if (flags[1]) {
                 __threadfence();
                 merge_parts<T, D, C::kConsumers>(
                     GlobalParts{p.slots, p.slot_floats, first, first_slot, G * D}, last - first + 1, G,
@@ -775,6 +883,8 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
             }
         }
     }
+    // no call's last kernel finishes before the ones it follows
+    if (kSuffix && !waited) pdl_wait();
     if (kLook && tid == 0) lookahead_claim(flags);   // the scout stops looking
     // no block of a cluster leaves while another may still store into it
     if constexpr (kCluster) cluster_sync_unaligned();

@@ -115,14 +115,24 @@ struct ClusterWalk {
     }
 };
 
-__device__ __forceinline__ int varlen_tiles(int len, int n_max, int tile)
+// Which part of a row's keys a walk covers: keys [key0, len) of a row whose
+// length is in [min_len, n_max], at least one tile of them (a row that ends
+// where its range begins still has a unit to finish).  {1, n_max, 0}: all keys.
+struct KeyRange {
+    int min_len, n_max, key0;
+};
+
+__device__ __forceinline__ int varlen_tiles(int len, const KeyRange &r, int tile)
 {
-    return (len >= 1 && len <= n_max) ? (len + tile - 1) / tile : 0;
+    if (len < r.min_len || len > r.n_max) return 0;
+    const int n = len - r.key0;
+    return n > tile ? (n + tile - 1) / tile : 1;
 }
 
 struct VarlenWalk {
     const int32_t *seqlens;
-    int B, top_k, n_max, tile;
+    KeyRange range;
+    int B, top_k, tile;
     long long t, t_end;
     int b, k, j, T, n;          // position: row, slot, tile in unit; row's tiles and keys
     long long unit_start;
@@ -138,7 +148,7 @@ struct VarlenWalk {
         s.whole = (j == 0 && run == T);
         s.unit_start = unit_start;
         s.unit_tiles = T;
-        s.n_keys = n;
+        s.n_keys = n - range.key0;
         t += run;
         j += run;
         if (j == T && t < t_end) {        // step to the next unit that has tiles
@@ -149,7 +159,7 @@ struct VarlenWalk {
                 do {
                     ++b;
                     n = seqlens[b];
-                    T = varlen_tiles(n, n_max, tile);
+                    T = varlen_tiles(n, range, tile);
                 } while (T == 0);
             }
         }
@@ -162,7 +172,7 @@ struct VarlenWalk {
 // the block calls it (it synchronises with __syncthreads).  Returns false if
 // this block has nothing to do.  scratch: shared, >= 2 * (NT/32) + 8 longs.
 template <int NT>
-__device__ bool varlen_plan(const int32_t *seqlens, int B, int top_k, int n_max, int tile,
+__device__ bool varlen_plan(const int32_t *seqlens, int B, int top_k, KeyRange range, int tile,
                             int max_blocks, long long *scratch, Schedule &S, VarlenWalk &w)
 {
     constexpr int kWarps = NT / 32;
@@ -174,7 +184,7 @@ __device__ bool varlen_plan(const int32_t *seqlens, int B, int top_k, int n_max,
     int tmax = 0;
     for (int r = tid; r < B; r += NT) {
         const int len = seqlens[r];
-        const int T = varlen_tiles(len, n_max, tile);
+        const int T = varlen_tiles(len, range, tile);
         if (T == 0 && blockIdx.x == 0) atomicOr(&g_sha_status, kStatusBadIndex);
         sum += (long long)top_k * T;
         tmax = max(tmax, T);
@@ -217,7 +227,7 @@ __device__ bool varlen_plan(const int32_t *seqlens, int B, int top_k, int n_max,
     for (int r0 = 0; r0 < B; r0 += NT) {
         const int r = r0 + tid;
         const int len = r < B ? seqlens[r] : 0;
-        const int T = r < B ? varlen_tiles(len, n_max, tile) : 0;
+        const int T = r < B ? varlen_tiles(len, range, tile) : 0;
         const long long val = (long long)top_k * T;
         long long incl = val;
 #pragma unroll
@@ -249,7 +259,7 @@ __device__ bool varlen_plan(const int32_t *seqlens, int B, int top_k, int n_max,
     w.seqlens = seqlens;
     w.B = B;
     w.top_k = top_k;
-    w.n_max = n_max;
+    w.range = range;
     w.tile = tile;
     w.t = t0;
     w.t_end = S.begin(blockIdx.x + 1);

@@ -194,6 +194,41 @@ sha_status_t sha_decode_paged(const void *q, const void *k_pages, const void *v_
                               float scale, void *out, sha_dtype_t dtype, void *stream);
 
 /*
+ * sha_decode_prefix -- sha_decode_paged for a batch whose rows all begin with the
+ * same prefix_len keys (a system prompt, a document, several samples of one
+ * prompt): the attention over the shared keys is computed once per KV head for
+ * all the rows that select it, and joined with each row's own part by the
+ * log-sum-exp rule.  The result is that of sha_decode_paged on the same keys, up
+ * to rounding.
+ *   prefix_table : device, int32 [ceil(prefix_len / page_size)]: the pages of keys
+ *                  [0, prefix_len); any row's block table begins with them
+ *   prefix_len   : >= 1, and <= max_pages * page_size
+ *   seqlens      : device, int32 [B], each in [prefix_len, max_pages * page_size]:
+ *                  row b attends to keys [0, seqlens[b]); of its block_table only
+ *                  the entries from prefix_len / page_size on are read
+ *   page_size    : a power of two >= 8, for every G (SHA_ERR_UNSUPPORTED otherwise);
+ *                  H_kv <= 1024, B * top_k <= 2^24
+ *   workspace    : device, 256-byte aligned, >= sha_decode_prefix_workspace_size
+ *                  bytes; scratch only (no contents carried between calls), owned
+ *                  by the caller; calls that share it must not overlap on the device
+ * Rows with a bad length, bad head ids and bad page ids are treated as in
+ * sha_decode_paged (a bad id in prefix_table leaves every unit's output
+ * unspecified).  The last page of the prefix may also hold keys of a row: they
+ * are not read as the prefix's.
+ */
+sha_status_t sha_decode_prefix(const void *q, const void *k_pages, const void *v_pages,
+                               const int32_t *batch_head_index, const int32_t *seqlens,
+                               const int32_t *block_table, const int32_t *prefix_table,
+                               int prefix_len, int B, int H_q, int H_kv, int num_pages,
+                               int page_size, int max_pages, int d, int top_k, float scale,
+                               void *out, sha_dtype_t dtype, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace sha_decode_prefix needs on the current device; 0 for sizes it
+ * would reject and for empty calls. */
+size_t sha_decode_prefix_workspace_size(int B, int H_q, int H_kv, int d, int top_k);
+
+/*
  * sha_decode_tokens -- head x token sparsity.  Polar Sparsity names the
  * combination of head sparsity with token sparsity as future work
  * (papernotes.org summary, "局限与展望"); this entry point is its plainest
