@@ -836,7 +836,7 @@ sha_status_t decode_impl(const void *q, const void *k, const void *v, const int3
     prm.n_sel = lay.n_sel;
     prm.min_len = 1;
     prm.key0 = 0;
-    prm.prefix = {};
+    prm.runs = nullptr;
     if (lay.strided) {
         StridedMaps kv;
         int vt, vh, vb;
@@ -861,14 +861,13 @@ sha_status_t decode_impl(const void *q, const void *k, const void *v, const int3
     return launch_decode<sha::kLayoutFixed>(prm, dtype, d, fma, look, dev, s);
 }
 
-// Workspace of a shared-prefix call: the suffix pass's arrival counters, the
-// units' references to their prefix parts, the suffix pass's partial states and
-// the prefix pass's.
+// Workspace of a shared-prefix call: the units' references to their runs over the
+// prefix and over their own keys, and the two passes' states.
 struct PrefixPlan {
     long long units;
     int row_tiles_max;           // row tiles the selection can need, at most
     int suffix_slot_floats, prefix_slot_floats;
-    size_t ref_at, suffix_at, prefix_at, bytes;
+    size_t runs_at, suffix_at, prefix_at, bytes;   // the references come first
 };
 
 template <int D>
@@ -884,9 +883,10 @@ PrefixPlan make_prefix_plan(int B, int H_q, int H_kv, int top_k, int num_sms)
     pl.suffix_slot_floats = (G * (D + 2) + 31) / 32 * 32;
     pl.prefix_slot_floats = C::kRows * (D + 2);
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
-    pl.ref_at = sha::kCounterBytes;
-    pl.suffix_at = pl.ref_at + up((size_t)pl.units * sizeof(int4));
-    pl.prefix_at = pl.suffix_at + up((size_t)2 * num_sms * pl.suffix_slot_floats * sizeof(float));
+    pl.runs_at = up((size_t)pl.units * sizeof(int4));
+    pl.suffix_at = pl.runs_at + up((size_t)pl.units * sizeof(int2));
+    pl.prefix_at = pl.suffix_at +
+                   up((size_t)(pl.units + num_sms) * pl.suffix_slot_floats * sizeof(float));
     pl.bytes = pl.prefix_at +
                up((size_t)(pl.row_tiles_max + num_sms) * pl.prefix_slot_floats * sizeof(float));
     return pl;
@@ -912,8 +912,8 @@ sha_status_t check_prefix_shape(int B, int H_q, int H_kv, int d, int top_k)
 
 template <typename T, int D>
 sha_status_t launch_prefix(const sha::PrefixParams &prm, const void *k, const void *v,
-                           const sha::DecodeParams &suffix, sha_dtype_t dtype, int num_sms,
-                           int dev, cudaStream_t stream)
+                           const sha::DecodeParams &suffix, const sha::PrefixMergeParams &merge,
+                           sha_dtype_t dtype, int num_sms, int dev, cudaStream_t stream)
 {
     using C = sha::PrefixConfig<D>;
     auto kernel = sha::sha_prefix_kernel<T, D>;
@@ -933,7 +933,14 @@ sha_status_t launch_prefix(const sha::PrefixParams &prm, const void *k, const vo
     cudaError_t e = launch_kernel(kernel, num_sms, C::kThreads, C::kSmemBytes, stream, prm, tm_k,
                                   tm_v);
     if (e != cudaSuccess) return launch_error(e);
-    return launch_gqa<T, D, sha::kLayoutSuffix, false>(suffix, dtype, dev, stream, nullptr);
+    st = launch_gqa<T, D, sha::kLayoutSuffix, false>(suffix, dtype, dev, stream, nullptr);
+    if (st != SHA_OK) return st;
+    const long long rows = (long long)prm.B * prm.top_k * (prm.H_q / prm.H_kv);
+    const int per_block = 256 / (D / 4);
+    e = launch_kernel(sha::sha_prefix_merge_kernel<T, D>, (int)((rows + per_block - 1) / per_block),
+                      256, 0, stream, merge);
+    if (e != cudaSuccess) return launch_error(e);
+    return SHA_OK;
 }
 
 __global__ void copy_probe_kernel(uint4 *__restrict__ dst, const uint4 *__restrict__ src,
@@ -1114,12 +1121,10 @@ sha_status_t sha_decode_prefix(const void *q, const void *k_pages, const void *v
     prm.page_size = page_size;
     prm.num_pages = num_pages;
     prm.scale_log2 = scale * 1.4426950408889634f;
-    prm.parts.ref = reinterpret_cast<int4 *>(ws + pl.ref_at);
+    prm.parts.ref = reinterpret_cast<int4 *>(ws);
     prm.parts.slots = reinterpret_cast<float *>(ws + pl.prefix_at);
     prm.parts.slot_floats = pl.prefix_slot_floats;
     prm.parts.slot_rows = pl.prefix_slot_floats / (d + 2);
-    prm.counters = reinterpret_cast<int *>(ws);
-    prm.num_counters = info->num_sms;
 
     sha::DecodeParams suf = {};
     suf.q = q;
@@ -1136,7 +1141,6 @@ sha_status_t sha_decode_prefix(const void *q, const void *k_pages, const void *v
     suf.sched.num_ctas = info->num_sms;      // the device plans an even cut of these
     suf.slots = reinterpret_cast<float *>(ws + pl.suffix_at);
     suf.slot_floats = pl.suffix_slot_floats;
-    suf.counters = prm.counters;
     suf.seqlens = seqlens;
     suf.block_table = block_table;
     suf.page_size = page_size;
@@ -1146,16 +1150,33 @@ sha_status_t sha_decode_prefix(const void *q, const void *k_pages, const void *v
     // the last box boundary at or before the prefix's end
     const int box = page_size < sha::GqaConfig<128>::kTile ? page_size : sha::GqaConfig<128>::kTile;
     suf.key0 = prefix_len / box * box;
-    suf.prefix = prm.parts;
+    suf.runs = reinterpret_cast<int2 *>(ws + pl.runs_at);
+
+    sha::PrefixMergeParams mrg;
+    mrg.idx = batch_head_index;
+    mrg.seqlens = seqlens;
+    mrg.out = out;
+    mrg.B = B;
+    mrg.H_q = H_q;
+    mrg.H_kv = H_kv;
+    mrg.top_k = top_k;
+    mrg.min_len = prefix_len;
+    mrg.max_len = suf.N_kv;
+    mrg.parts = prm.parts;
+    mrg.runs = suf.runs;
+    mrg.slots = suf.slots;
+    mrg.slot_floats = suf.slot_floats;
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int sms = info->num_sms;
     if (dtype == SHA_FP16)
-        return d == 128 ? launch_prefix<__half, 128>(prm, k_pages, v_pages, suf, dtype, sms, dev, s)
-                        : launch_prefix<__half, 64>(prm, k_pages, v_pages, suf, dtype, sms, dev, s);
-    return d == 128
-               ? launch_prefix<__nv_bfloat16, 128>(prm, k_pages, v_pages, suf, dtype, sms, dev, s)
-               : launch_prefix<__nv_bfloat16, 64>(prm, k_pages, v_pages, suf, dtype, sms, dev, s);
+        return d == 128
+                   ? launch_prefix<__half, 128>(prm, k_pages, v_pages, suf, mrg, dtype, sms, dev, s)
+                   : launch_prefix<__half, 64>(prm, k_pages, v_pages, suf, mrg, dtype, sms, dev, s);
+    return d == 128 ? launch_prefix<__nv_bfloat16, 128>(prm, k_pages, v_pages, suf, mrg, dtype, sms,
+                                                        dev, s)
+                    : launch_prefix<__nv_bfloat16, 64>(prm, k_pages, v_pages, suf, mrg, dtype, sms,
+                                                       dev, s);
 }
 
 size_t sha_decode_workspace_size(int B, int H_q, int H_kv, int N_kv, int d, int top_k,

@@ -148,60 +148,6 @@ __device__ __forceinline__ uint32_t swizzled(uint32_t tile, int key, int chunk)
     return tile + box * C::kBoxBytes + key * 128 + ((c ^ (key & 7)) << 4);
 }
 
-// Four neighbouring elements of an output row being put together from partial
-// states (O, m, l) by the log-sum-exp rule, in the order they are folded in.
-template <typename T>
-struct FoldedRow {
-    float4 O;
-    float M, L;
-
-    __device__ __forceinline__ void start(float m, float l)
-    {
-        O = make_float4(0.f, 0.f, 0.f, 0.f);
-        M = m;
-        L = l;
-    }
-    // a term already in terms of M (a warp's share of this block's state)
-    __device__ __forceinline__ void add(float w, float2 a, float2 b)
-    {
-        O.x = fmaf(w, a.x, O.x);
-        O.y = fmaf(w, a.y, O.y);
-        O.z = fmaf(w, b.x, O.z);
-        O.w = fmaf(w, b.y, O.w);
-    }
-    __device__ __forceinline__ void fold(float m, float l, float4 x)
-    {
-        const float top = fmaxf(M, m);
-        const float ref = top == -INFINITY ? 0.f : top;
-        const float a = exp2f(M - ref), b = exp2f(m - ref);
-        O.x = fmaf(b, x.x, a * O.x);
-        O.y = fmaf(b, x.y, a * O.y);
-        O.z = fmaf(b, x.z, a * O.z);
-        O.w = fmaf(b, x.w, a * O.w);
-        L = fmaf(b, l, a * L);
-        M = top;
-    }
-    __device__ __forceinline__ void fold_prefix(const PrefixParts &p, const int4 &ref, int row,
-                                                int c, int D)
-    {
-        const float *slot = p.slots + (size_t)ref.x * p.slot_floats;
-        const int r = ref.z + row;
-#pragma unroll 4
-        for (int i = 0; i < ref.y; ++i, slot += p.slot_floats) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(
-                slot + (size_t)p.slot_rows * D + 2 * r));
-            const float4 x =
-                __ldcg(reinterpret_cast<const float4 *>(slot + (size_t)r * D + c));
-            fold(ml.x, ml.y, x);
-        }
-    }
-    __device__ __forceinline__ void store(T *out)
-    {
-        *reinterpret_cast<uint2 *>(out) =
-            make_uint2(pack2<T>(O.x / L, O.y / L), pack2<T>(O.z / L, O.w / L));
-    }
-};
-
 template <typename T, int D, int kLayout, bool kLook>
 __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == kLayoutTokens), 1)
     sha_gqa_decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm_k,
@@ -264,9 +210,9 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
                      : "memory");
     }
     // inputs, workspace and the output may come from the previous kernel.  The
-    // kernel before a suffix pass is the prefix pass of the same call: it started
-    // after everything before it had finished, and writes nothing that is read
-    // before the first unit is put together, where it is waited for.
+    // kernel before a suffix pass is the prefix pass of the same call: it lets this
+    // one start only after everything before it has finished, and nothing that it
+    // writes is read or overwritten here, so it is only waited for at the end.
     if constexpr (!kSuffix) pdl_wait();
     pdl_launch_dependents();
     if constexpr (kCluster) cluster_wait();
@@ -521,8 +467,6 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
 
     Walk wk = walk;
     Seg seg;
-    bool waited = false;   // suffix: the prefix pass has finished
-    (void)waited;
     int n_done = 0;   // clustered cut: units this block has finished (its buffers' parity)
     for (bool first_seg = true; wk.next(seg); first_seg = false) {
         const long long u = seg.unit;
@@ -694,7 +638,7 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
         // blocks first..last share a split unit; the one the block ends with may
         // be finished on chip
         int first = 0, last = 0, first_slot = 0;
-        if (!kCluster && !seg.whole) unit_parts(S, seg, first, last, first_slot);
+        if (!kCluster && (kSuffix || !seg.whole)) unit_parts(S, seg, first, last, first_slot);
         int la_parts = 0;
         if constexpr (kLook)
             if (wk.t >= wk.t_end) la_parts = lookahead_parts(seg, first, last, max_partners);
@@ -730,13 +674,13 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
                     : p.slots ? p.slots + (size_t)(2 * blockIdx.x + (first_seg ? 0 : 1)) *
                                               p.slot_floats
                               : nullptr;
-        // the unit's parts over a shared prefix: the kernel that computed them has
-        // run beside this one's first streaming, and is waited for here
-        int4 pref = make_int4(0, 0, 0, 0);
+        // a suffix pass leaves every run of a unit's tiles, whole or not, to be put
+        // together with the unit's part over the prefix: run (unit u, block c) in
+        // slot u + c, which the next run exceeds, u or c or both having advanced
         if constexpr (kSuffix) {
-            if (!waited) pdl_wait();
-            waited = true;
-            pref = __ldcg(p.prefix.ref + u);
+            slot = p.slots + (size_t)(u + blockIdx.x) * p.slot_floats;
+            if (seg.first_tile == 0 && tid == 0)
+                p.runs[u] = make_int2((int)u + (int)blockIdx.x, last - first + 1);
         }
         // under the clustered cut, a unit that is not whole here is shared by
         // the cluster's blocks
@@ -770,25 +714,8 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
                                cr[C::kConsumerWarps + 1], &cbar[buf]);
             }
         } else if (!aborted) {
-            if (kSuffix && seg.whole) {
-                // four elements of a row per thread, the prefix's parts folded in
-                for (int e = 4 * tid; e < G * D; e += 4 * C::kConsumers) {
-                    const int row = e / D, c = e - row * D;
-                    const float *cr = cw + row * C::kCombineFloats;
-                    FoldedRow<T> f;
-                    f.start(cr[C::kConsumerWarps], cr[C::kConsumerWarps + 1]);
-#pragma unroll
-                    for (int w = 0; w < C::kConsumerWarps; ++w) {
-                        const float *st = wstate + w * C::kStateFloats + row * (D + 2) + c;
-                        f.add(cr[w], *reinterpret_cast<const float2 *>(st),
-                              *reinterpret_cast<const float2 *>(st + 2));
-                    }
-                    f.fold_prefix(p.prefix, pref, row, c, D);
-                    f.store(out_g + e);
-                }
-            }
             // two neighbouring elements of a row per thread (D is even)
-            for (int e = kSuffix && seg.whole ? G * D : 2 * tid; e < G * D; e += 2 * C::kConsumers) {
+            for (int e = 2 * tid; e < G * D; e += 2 * C::kConsumers) {
                 const int row = e / D, c = e - row * D;
                 const float *cr = cw + row * C::kCombineFloats;
                 float2 O = make_float2(0.f, 0.f);
@@ -800,7 +727,7 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
                     O.y = fmaf(cr[w], x.y, O.y);
                 }
                 const float L = cr[C::kConsumerWarps + 1];
-                if (seg.whole) {
+                if (!kSuffix && seg.whole) {
                     *reinterpret_cast<uint32_t *>(out_g + e) = pack2<T>(O.x / L, O.y / L);
                 } else {
                     *reinterpret_cast<float2 *>(slot + e) = O;
@@ -810,7 +737,7 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
                     }
                 }
             }
-            if (!kCluster && !seg.whole && !on_chip) __threadfence();
+            if (!kCluster && !kSuffix && !seg.whole && !on_chip) __threadfence();
         }
         named_barrier(1, C::kConsumers);
 
@@ -847,7 +774,7 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
                                                   G, out_g, wstate, tid);
                 if (tid == 0) p.counters[first] = 0;
             }
-        } else if (!seg.whole) {
+        } else if (!kSuffix && !seg.whole) {
             if (tid == 0) {
                 int merge = 0;
                 if (!flags[0]) {
@@ -857,24 +784,7 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
                 flags[1] = merge;
             }
             named_barrier(1, C::kConsumers);
-            if (kSuffix && flags[1]) {
-                __threadfence();
-                const int parts = last - first + 1;
-                for (int e = 4 * tid; e < G * D; e += 4 * C::kConsumers) {
-                    const int row = e / D, c = e - row * D;
-                    FoldedRow<T> f;
-                    f.start(-INFINITY, 0.f);
-                    for (int i = 0; i < parts; ++i) {
-                        const float *part =
-                            p.slots + (size_t)merge_slot(first, first_slot, i) * p.slot_floats;
-                        f.fold(__ldcg(part + G * D + row), __ldcg(part + G * D + G + row),
-                               __ldcg(reinterpret_cast<const float4 *>(part + e)));
-                    }
-                    f.fold_prefix(p.prefix, pref, row, c, D);
-                    f.store(out_g + e);
-                }
-                if (tid == 0) p.counters[first] = 0;
-            } else if (flags[1]) {
+            if (flags[1]) {
                 __threadfence();
                 merge_parts<T, D, C::kConsumers>(
                     GlobalParts{p.slots, p.slot_floats, first, first_slot, G * D}, last - first + 1, G,
@@ -883,8 +793,8 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
             }
         }
     }
-    // no call's last kernel finishes before the ones it follows
-    if (kSuffix && !waited) pdl_wait();
+    // the prefix pass before this one has finished, too, when this one has
+    if constexpr (kSuffix) pdl_wait();
     if (kLook && tid == 0) lookahead_claim(flags);   // the scout stops looking
     // no block of a cluster leaves while another may still store into it
     if constexpr (kCluster) cluster_sync_unaligned();

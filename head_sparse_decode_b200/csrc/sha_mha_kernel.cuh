@@ -43,17 +43,6 @@
 
 namespace sha {
 
-// What the shared-prefix pass (sha_prefix_kernel.cuh) leaves for the rest of the
-// call.  Unit u's part over the prefix lies in ref[u].y consecutive slots from
-// slot ref[u].x on, one per run of the prefix's key tiles, its G rows at rows
-// ref[u].z .. of each; a slot holds O (rows x d, unnormalised), then (m, l) per
-// row, m in log2 units.
-struct PrefixParts {
-    int4 *ref;
-    float *slots;
-    int slot_floats, slot_rows;
-};
-
 struct DecodeParams {
     const void *q;
     const void *k;
@@ -80,10 +69,11 @@ struct DecodeParams {
     const int32_t *tokens;
     int n_sel;
     // keys behind a shared prefix (kLayoutSuffix): row b's own keys are [min_len,
-    // seqlens[b]) of its pages, streamed from key0 <= min_len on, a box boundary;
-    // prefix holds the shared part's results
+    // seqlens[b]) of its pages, streamed from key0 <= min_len on, a box boundary.
+    // Nothing is finished there: unit u's runs of tiles leave their states in the
+    // runs[u].y slots from runs[u].x on
     int min_len, key0;
-    PrefixParts prefix;
+    int2 *runs;
 
     __device__ __forceinline__ KeyRange keys() const { return {min_len, N_kv, key0}; }
 };
