@@ -17,6 +17,7 @@
 #include "sha_prefix_kernel.cuh"
 #include "sha_schedule.cuh"
 #include "sha_select_kernel.cuh"
+#include "sha_suffix_kernel.cuh"
 
 namespace {
 
@@ -550,7 +551,7 @@ sha_status_t launch_gqa(const sha::DecodeParams &prm, sha_dtype_t dtype, int dev
         return SHA_OK;
     }
     // a padded cache: [B*H_kv][N_kv][d]; a page pool: [num_pages*H_kv][page_size][d]
-    const bool paged = sha::layout_paged(kLayout);
+    const bool paged = kLayout == sha::kLayoutPaged;
     const long long planes = paged ? (long long)prm.num_pages * prm.H_kv : (long long)prm.B * prm.H_kv;
     const int rows = paged ? prm.page_size : prm.N_kv;
     const int box_rows = paged && prm.page_size < C::kTile ? prm.page_size : C::kTile;
@@ -834,9 +835,6 @@ sha_status_t decode_impl(const void *q, const void *k, const void *v, const int3
     prm.batch_dim = 2;
     prm.tokens = lay.tokens;
     prm.n_sel = lay.n_sel;
-    prm.min_len = 1;
-    prm.key0 = 0;
-    prm.runs = nullptr;
     if (lay.strided) {
         StridedMaps kv;
         int vt, vh, vb;
@@ -886,7 +884,8 @@ PrefixPlan make_prefix_plan(int B, int H_q, int H_kv, int top_k, int num_sms)
     pl.runs_at = up((size_t)pl.units * sizeof(int4));
     pl.suffix_at = pl.runs_at + up((size_t)pl.units * sizeof(int2));
     pl.prefix_at = pl.suffix_at +
-                   up((size_t)(pl.units + num_sms) * pl.suffix_slot_floats * sizeof(float));
+                   up((size_t)(pl.units + (long long)num_sms * sha::SuffixConfig<D>::kWorkers) *
+                      pl.suffix_slot_floats * sizeof(float));
     pl.bytes = pl.prefix_at +
                up((size_t)(pl.row_tiles_max + num_sms) * pl.prefix_slot_floats * sizeof(float));
     return pl;
@@ -912,15 +911,26 @@ sha_status_t check_prefix_shape(int B, int H_q, int H_kv, int d, int top_k)
 
 template <typename T, int D>
 sha_status_t launch_prefix(const sha::PrefixParams &prm, const void *k, const void *v,
-                           const sha::DecodeParams &suffix, const sha::PrefixMergeParams &merge,
+                           const sha::SuffixParams &suffix, const sha::PrefixMergeParams &merge,
                            sha_dtype_t dtype, int num_sms, int dev, cudaStream_t stream)
 {
     using C = sha::PrefixConfig<D>;
+    using Suffix = sha::SuffixConfig<D>;
     auto kernel = sha::sha_prefix_kernel<T, D>;
+    const bool tall = prm.H_q / prm.H_kv > 8;
+    auto suffix_kernel = tall ? sha::sha_suffix_kernel<T, D, 2> : sha::sha_suffix_kernel<T, D, 1>;
     static std::atomic<bool> configured[kMaxDevices];
     if (!configured[dev].load(std::memory_order_acquire)) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              C::kSmemBytes);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(sha::sha_suffix_kernel<T, D, 1>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     Suffix::kSmemBytes);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(sha::sha_suffix_kernel<T, D, 2>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     Suffix::kSmemBytes);
         if (e != cudaSuccess) return launch_error(e);
         configured[dev].store(true, std::memory_order_release);
     }
@@ -933,8 +943,15 @@ sha_status_t launch_prefix(const sha::PrefixParams &prm, const void *k, const vo
     cudaError_t e = launch_kernel(kernel, num_sms, C::kThreads, C::kSmemBytes, stream, prm, tm_k,
                                   tm_v);
     if (e != cudaSuccess) return launch_error(e);
-    st = launch_gqa<T, D, sha::kLayoutSuffix, false>(suffix, dtype, dev, stream, nullptr);
-    if (st != SHA_OK) return st;
+    const int suffix_box = prm.page_size < Suffix::kStage ? prm.page_size : Suffix::kStage;
+    if (suffix_box != box_rows) {
+        st = kv_tensor_map(&tm_k, k, dtype, D, prm.page_size, planes, suffix_box);
+        if (st == SHA_OK) st = kv_tensor_map(&tm_v, v, dtype, D, prm.page_size, planes, suffix_box);
+        if (st != SHA_OK) return st;
+    }
+    e = launch_kernel(suffix_kernel, num_sms, Suffix::kThreads, Suffix::kSmemBytes, stream, suffix,
+                      tm_k, tm_v);
+    if (e != cudaSuccess) return launch_error(e);
     const long long rows = (long long)prm.B * prm.top_k * (prm.H_q / prm.H_kv);
     const int per_block = 256 / (D / 4);
     e = launch_kernel(sha::sha_prefix_merge_kernel<T, D>, (int)((rows + per_block - 1) / per_block),
@@ -1126,30 +1143,28 @@ sha_status_t sha_decode_prefix(const void *q, const void *k_pages, const void *v
     prm.parts.slot_floats = pl.prefix_slot_floats;
     prm.parts.slot_rows = pl.prefix_slot_floats / (d + 2);
 
-    sha::DecodeParams suf = {};
+    sha::SuffixParams suf;
     suf.q = q;
-    suf.k = k_pages;
-    suf.v = v_pages;
     suf.idx = batch_head_index;
-    suf.out = out;
+    suf.seqlens = seqlens;
+    suf.block_table = block_table;
     suf.B = B;
     suf.H_q = H_q;
     suf.H_kv = H_kv;
-    suf.N_kv = max_pages * page_size;
     suf.top_k = top_k;
-    suf.scale_log2 = prm.scale_log2;
-    suf.sched.num_ctas = info->num_sms;      // the device plans an even cut of these
-    suf.slots = reinterpret_cast<float *>(ws + pl.suffix_at);
-    suf.slot_floats = pl.suffix_slot_floats;
-    suf.seqlens = seqlens;
-    suf.block_table = block_table;
-    suf.page_size = page_size;
+    suf.min_len = prefix_len;
+    suf.max_len = max_pages * page_size;
+    // the last box boundary at or before the prefix's end
+    const int box = page_size < sha::SuffixConfig<128>::kStage ? page_size
+                                                               : sha::SuffixConfig<128>::kStage;
+    suf.key0 = prefix_len / box * box;
+    suf.page_shift = 0;
+    while (1 << suf.page_shift < page_size) ++suf.page_shift;
     suf.max_pages = max_pages;
     suf.num_pages = num_pages;
-    suf.min_len = prefix_len;
-    // the last box boundary at or before the prefix's end
-    const int box = page_size < sha::GqaConfig<128>::kTile ? page_size : sha::GqaConfig<128>::kTile;
-    suf.key0 = prefix_len / box * box;
+    suf.scale_log2 = prm.scale_log2;
+    suf.slots = reinterpret_cast<float *>(ws + pl.suffix_at);
+    suf.slot_floats = pl.suffix_slot_floats;
     suf.runs = reinterpret_cast<int2 *>(ws + pl.runs_at);
 
     sha::PrefixMergeParams mrg;
@@ -1161,7 +1176,7 @@ sha_status_t sha_decode_prefix(const void *q, const void *k_pages, const void *v
     mrg.H_kv = H_kv;
     mrg.top_k = top_k;
     mrg.min_len = prefix_len;
-    mrg.max_len = suf.N_kv;
+    mrg.max_len = suf.max_len;
     mrg.parts = prm.parts;
     mrg.runs = suf.runs;
     mrg.slots = suf.slots;

@@ -319,6 +319,15 @@ template <> struct Elem<__nv_bfloat16> {
     }
 };
 
+// 2^x by the hardware instruction: at most 2 ulp off, subnormals flushed to zero
+// (weights below 2^-126 of the largest).
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Two fp32 values rounded to T and packed low/high into one 32-bit register.
 template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
 template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi)

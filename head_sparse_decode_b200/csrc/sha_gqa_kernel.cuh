@@ -155,7 +155,6 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
 {
     constexpr bool kVarlen = layout_varlen(kLayout);
     constexpr bool kCluster = kLayout == kLayoutCluster;
-    constexpr bool kSuffix = kLayout == kLayoutSuffix;
     using Walk = typename std::conditional<
         kVarlen, VarlenWalk,
         typename std::conditional<kCluster, ClusterWalk, UniformWalk>::type>::type;
@@ -209,23 +208,18 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v))
                      : "memory");
     }
-    // inputs, workspace and the output may come from the previous kernel.  The
-    // kernel before a suffix pass is the prefix pass of the same call: it lets this
-    // one start only after everything before it has finished, and nothing that it
-    // writes is read or overwritten here, so it is only waited for at the end.
-    if constexpr (!kSuffix) pdl_wait();
+    // inputs, workspace and the output may come from the previous kernel
+    pdl_wait();
     pdl_launch_dependents();
     if constexpr (kCluster) cluster_wait();
 
     Schedule S = p.sched;
     Walk walk;
     if constexpr (kVarlen) {
-        if (!varlen_plan<C::threads(kLook)>(p.seqlens, p.B, p.top_k, p.keys(), C::kTile, gridDim.x,
+        if (!varlen_plan<C::threads(kLook)>(p.seqlens, p.B, p.top_k, p.N_kv, C::kTile, gridDim.x,
                                       reinterpret_cast<long long *>(smem + C::kPlanOffset), S,
-                                      walk)) {
-            if constexpr (kSuffix) pdl_wait();
+                                      walk))
             return;
-        }
     } else if constexpr (kCluster) {
         walk.start(S, (long long)p.B * p.top_k, p.N_kv);
     } else {
@@ -255,7 +249,7 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
     if (gw >= 0) {
         // A paged cache needs several page ids per tile: the whole warp gathers
         // them (one page box per lane).  Otherwise one lane drives the pipeline.
-        constexpr bool kWarpProducer = layout_paged(kLayout) || kLayout == kLayoutTokens;
+        constexpr bool kWarpProducer = kLayout == kLayoutPaged || kLayout == kLayoutTokens;
         if (!kWarpProducer && lane != 0) {
             if constexpr (kCluster) cluster_sync_unaligned();
             return;
@@ -305,7 +299,7 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
                 }
                 if constexpr (kWarpProducer) go = __shfl_sync(0xffffffffu, go, 0);
                 if (!go) { ok = false; break; }
-                if constexpr (layout_paged(kLayout)) {
+                if constexpr (kLayout == kLayoutPaged) {
                     // boxes of min(page_size, tile) keys, each inside one page,
                     // landing at 1 KiB-aligned rows of the swizzled tile
                     const int n0 = j * C::kTile;
@@ -318,7 +312,7 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
                     __syncwarp();
                     const int32_t *bt = p.block_table + (size_t)b * p.max_pages;
                     for (int c = lane; c < chunks; c += 32) {
-                        const int key = (kSuffix ? p.key0 : 0) + n0 + c * box_rows;
+                        const int key = n0 + c * box_rows;
                         const int pi = key / p.page_size, off = key - pi * p.page_size;
                         int page = bt[pi];
                         if ((unsigned)page >= (unsigned)p.num_pages) {
@@ -511,18 +505,16 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
                 const uint32_t kt = k_base + stage * C::kTileBytes;
                 const uint32_t vt = v_base + stage * C::kTileBytes;
                 const int rows = min(C::kTile, seg.n_keys - j * C::kTile);
-                // a suffix's first tile begins with the prefix's last keys
-                const int lo = kSuffix && j == 0 ? p.min_len - p.key0 : 0;
                 if constexpr (kVarlen) {
                     // keys past this row's length but inside the cache hold stale
                     // values: zero this warp's V rows there (0 * NaN would poison P V)
-                    if (rows < C::kTile || lo > 0) {
+                    if (rows < C::kTile) {
                         unsigned char *vtile = v_ring + stage * C::kTileBytes;
                         for (int i = lane; i < C::kSlices * 16 * C::kBoxes * 8; i += 32) {
                             const int chunk = i & 7, bx = (i >> 3) % C::kBoxes;
                             const int rr = (i >> 3) / C::kBoxes;      // 0 .. kSlices*16-1
                             const int key = (rr >> 4) * 64 + warp * C::kKeysPerWarp + (rr & 15);
-                            if (key >= rows || key < lo)
+                            if (key >= rows)
                                 *reinterpret_cast<uint4 *>(vtile + bx * C::kBoxBytes + key * 128 +
                                                            chunk * 16) = make_uint4(0, 0, 0, 0);
                         }
@@ -558,9 +550,7 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
                         for (int e = 0; e < 4; ++e) {
                             const int key = sl * 64 + warp * C::kKeysPerWarp + nt * 8 + qd * 2 +
                                             (e & 1);
-                            s[sl][nt][e] = key < rows && key >= lo
-                                               ? s[sl][nt][e] * p.scale_log2
-                                               : -INFINITY;
+                            s[sl][nt][e] = key < rows ? s[sl][nt][e] * p.scale_log2 : -INFINITY;
                             mt[e >> 1] = fmaxf(mt[e >> 1], s[sl][nt][e]);
                         }
                 float alpha[2], ref[2];
@@ -638,7 +628,7 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
         // blocks first..last share a split unit; the one the block ends with may
         // be finished on chip
         int first = 0, last = 0, first_slot = 0;
-        if (!kCluster && (kSuffix || !seg.whole)) unit_parts(S, seg, first, last, first_slot);
+        if (!kCluster && !seg.whole) unit_parts(S, seg, first, last, first_slot);
         int la_parts = 0;
         if constexpr (kLook)
             if (wk.t >= wk.t_end) la_parts = lookahead_parts(seg, first, last, max_partners);
@@ -674,14 +664,6 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
                     : p.slots ? p.slots + (size_t)(2 * blockIdx.x + (first_seg ? 0 : 1)) *
                                               p.slot_floats
                               : nullptr;
-        // a suffix pass leaves every run of a unit's tiles, whole or not, to be put
-        // together with the unit's part over the prefix: run (unit u, block c) in
-        // slot u + c, which the next run exceeds, u or c or both having advanced
-        if constexpr (kSuffix) {
-            slot = p.slots + (size_t)(u + blockIdx.x) * p.slot_floats;
-            if (seg.first_tile == 0 && tid == 0)
-                p.runs[u] = make_int2((int)u + (int)blockIdx.x, last - first + 1);
-        }
         // under the clustered cut, a unit that is not whole here is shared by
         // the cluster's blocks
         bool shared = false;
@@ -727,7 +709,7 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
                     O.y = fmaf(cr[w], x.y, O.y);
                 }
                 const float L = cr[C::kConsumerWarps + 1];
-                if (!kSuffix && seg.whole) {
+                if (seg.whole) {
                     *reinterpret_cast<uint32_t *>(out_g + e) = pack2<T>(O.x / L, O.y / L);
                 } else {
                     *reinterpret_cast<float2 *>(slot + e) = O;
@@ -737,7 +719,7 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
                     }
                 }
             }
-            if (!kCluster && !kSuffix && !seg.whole && !on_chip) __threadfence();
+            if (!kCluster && !seg.whole && !on_chip) __threadfence();
         }
         named_barrier(1, C::kConsumers);
 
@@ -774,7 +756,7 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
                                                   G, out_g, wstate, tid);
                 if (tid == 0) p.counters[first] = 0;
             }
-        } else if (!kSuffix && !seg.whole) {
+        } else if (!seg.whole) {
             if (tid == 0) {
                 int merge = 0;
                 if (!flags[0]) {
@@ -793,8 +775,6 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
             }
         }
     }
-    // the prefix pass before this one has finished, too, when this one has
-    if constexpr (kSuffix) pdl_wait();
     if (kLook && tid == 0) lookahead_claim(flags);   // the scout stops looking
     // no block of a cluster leaves while another may still store into it
     if constexpr (kCluster) cluster_sync_unaligned();

@@ -68,14 +68,6 @@ struct DecodeParams {
     // u * n_sel + n_sel) of its head (positions in [0, N_kv))
     const int32_t *tokens;
     int n_sel;
-    // keys behind a shared prefix (kLayoutSuffix): row b's own keys are [min_len,
-    // seqlens[b]) of its pages, streamed from key0 <= min_len on, a box boundary.
-    // Nothing is finished there: unit u's runs of tiles leave their states in the
-    // runs[u].y slots from runs[u].x on
-    int min_len, key0;
-    int2 *runs;
-
-    __device__ __forceinline__ KeyRange keys() const { return {min_len, N_kv, key0}; }
 };
 
 // How K/V of a unit are found: one padded [N_kv] block per (b, h) with every
@@ -93,22 +85,14 @@ enum : int {
     kLayoutCluster = 5,
     // the padded layout, each unit restricted to a listed subset of its keys,
     // gathered row by row (grouped kernel only)
-    kLayoutTokens = 6,
-    // pages of a shared pool, each row's keys behind a prefix that all rows share
-    // and whose part sha_prefix_kernel.cuh has computed (grouped kernel only)
-    kLayoutSuffix = 7
+    kLayoutTokens = 6
 };
 
 // Layouts whose rows have their own lengths (planned on the device) and that
 // read K/V through strided 4-D tensor maps.
 constexpr bool layout_varlen(int layout)
 {
-    return layout == kLayoutVarlen || layout == kLayoutPaged || layout == kLayoutStridedVarlen ||
-           layout == kLayoutSuffix;
-}
-constexpr bool layout_paged(int layout)
-{
-    return layout == kLayoutPaged || layout == kLayoutSuffix;
+    return layout == kLayoutVarlen || layout == kLayoutPaged || layout == kLayoutStridedVarlen;
 }
 constexpr bool layout_strided(int layout)
 {
@@ -228,7 +212,7 @@ __global__ void __launch_bounds__(MhaConfig<D>::threads(kLook), SHA_MHA_BLOCKS_P
     Schedule S = p.sched;
     Walk walk;
     if constexpr (kVarlen) {
-        if (!varlen_plan<C::threads(kLook)>(p.seqlens, p.B, p.top_k, p.keys(), C::kTile, gridDim.x,
+        if (!varlen_plan<C::threads(kLook)>(p.seqlens, p.B, p.top_k, p.N_kv, C::kTile, gridDim.x,
                                       reinterpret_cast<long long *>(smem + C::kPlanOffset), S,
                                       walk))
             return;

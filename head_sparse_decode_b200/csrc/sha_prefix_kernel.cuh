@@ -7,7 +7,7 @@
 // unit divides its traffic by R_h (about B * top_k / H_kv).  The softmax over a
 // row's whole key range is put together from its two parts by the log-sum-exp
 // rule: this kernel leaves (O, m, l) of each query row over [0, P), the suffix
-// pass (sha_gqa_kernel.cuh, kLayoutSuffix) those over the row's own keys, and a
+// pass (sha_suffix_kernel.cuh) those over the row's own keys, and a
 // third kernel, wide enough to keep many loads in flight, puts them together.  (Put
 // together by the suffix pass at the end of each unit they cost it 3 us a unit, its
 // ring standing full meanwhile: 113 us against 78 for the OPT-66B-shaped batch.)
@@ -119,13 +119,6 @@ struct PrefixConfig {
 // (log2 units): P stays below 2^8, far inside fp16.
 constexpr float kPrefixSlack = 8.f;
 
-__device__ __forceinline__ float exp2_approx(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // First row tile of every head (start[H_kv] = all of them), from the histogram
 // of the selection.  All threads of the block; ends with a barrier.
 template <int NT>
@@ -136,9 +129,13 @@ __device__ __forceinline__ void prefix_row_tiles(const PrefixParams &p, int unit
     for (int h = tid; h <= p.H_kv; h += NT) start[h] = 0;
     __syncthreads();
     const int units = p.B * p.top_k;
-    for (int u = tid; u < units; u += NT) {
-        const int h = p.idx[u];
-        if ((unsigned)h < (unsigned)p.H_kv) atomicAdd(&start[h], 1);
+    for (int u0 = tid; u0 < units; u0 += 4 * NT) {
+        int h[4];                                    // four loads on the way at a time
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = u0 + i * NT < units ? p.idx[u0 + i * NT] : -1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if ((unsigned)h[i] < (unsigned)p.H_kv) atomicAdd(&start[h[i]], 1);
     }
     __syncthreads();
     if (tid < 32) {                                  // counts -> exclusive sums of row tiles
@@ -157,6 +154,36 @@ __device__ __forceinline__ void prefix_row_tiles(const PrefixParams &p, int unit
         }
     }
     __syncthreads();
+}
+
+// How the row tiles are cut over `blocks` blocks.  Beginning a run (its list, its
+// queries, its state written out) takes a block about as long as kRunTiles key
+// tiles, so whole row tiles, or equal pieces of them, go to the blocks where the
+// busiest then has no more to do than under the even cut, which gives most blocks
+// two runs.  (OPT-66B-shaped, 72 row tiles of 15 key tiles: 2 pieces of 7 or 8
+// each, 144 runs, against 219.)
+constexpr int kRunTiles = 3;
+__device__ __forceinline__ void prefix_cut(Schedule &S, int row_tiles, int blocks)
+{
+    const int tpu = S.tiles_per_unit;
+    S.total_tiles = (long long)row_tiles * tpu;
+    S.pieces = 0;
+    S.num_ctas = S.total_tiles < blocks ? (int)S.total_tiles : blocks;
+    if (row_tiles == 0) return;
+    const long long even = (S.total_tiles + S.num_ctas - 1) / S.num_ctas + 2 * kRunTiles;
+    if (row_tiles <= blocks) {
+        const int p = min(blocks / row_tiles, tpu);
+        if ((tpu + p - 1) / p + kRunTiles <= even) {
+            S.pieces = p;
+            S.num_ctas = row_tiles * p;
+        }
+    } else {
+        const int whole = (row_tiles + blocks - 1) / blocks;
+        if ((long long)whole * (tpu + kRunTiles) <= even) {
+            S.pieces = 1;
+            S.num_ctas = blocks;
+        }
+    }
 }
 
 // The head of row tile r: the last h with start[h] <= r among those that have tiles.
@@ -239,9 +266,7 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
     const int key_tiles = (p.keys + C::kTile - 1) / C::kTile;
     Schedule S;
     S.tiles_per_unit = key_tiles;                    // a "unit" here is a row tile
-    S.total_tiles = (long long)start[p.H_kv] * key_tiles;
-    S.pieces = 0;
-    S.num_ctas = S.total_tiles < gridDim.x ? (int)S.total_tiles : (int)gridDim.x;
+    prefix_cut(S, start[p.H_kv], (int)gridDim.x);
     UniformWalk wk;
     wk.S = S;
     wk.t = wk.t_end = 0;
@@ -409,24 +434,34 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
             // this row tile's units: those of the head's units, in order, that the
             // tiles before it have not taken
             const int rank0 = (rt - start[h]) * units_per_tile;
-            int seen = 0;
             named_barrier(1, C::kSoftmax);                // the last run's list has been read
-            for (int u0 = 0; u0 < units && seen < rank0 + units_per_tile; u0 += C::kSoftmax) {
-                const int u = u0 + stid;
-                const bool hit = u < units && p.idx[u] == h;
-                const unsigned votes = __ballot_sync(FULL, hit);
-                if (lane == 0) warp_counts[swarp] = __popc(votes);
-                named_barrier(1, C::kSoftmax);
-                int before = seen, total = 0;
-                for (int w = 0; w < C::kSoftmax / 32; ++w) {
-                    if (w < swarp) before += warp_counts[w];
-                    total += warp_counts[w];
-                }
-                const int rank = before + __popc(votes & ((1u << lane) - 1)) - rank0;
-                if (hit && rank >= 0 && rank < units_per_tile) unit_list[rank] = u;
-                seen += total;
-                named_barrier(1, C::kSoftmax);
+            // (a contiguous share of the units per thread: count, scan, then place)
+            const int per = (units + C::kSoftmax - 1) / C::kSoftmax;
+            const int share0 = min(stid * per, units), share1 = min(share0 + per, units);
+            int mine = 0;
+#pragma unroll 8
+            for (int u = share0; u < share1; ++u) mine += p.idx[u] == h;
+            int incl = mine;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int x = __shfl_up_sync(FULL, incl, off);
+                if (lane >= off) incl += x;
             }
+            if (lane == 31) warp_counts[swarp] = incl;
+            named_barrier(1, C::kSoftmax);
+            int rank = incl - mine - rank0, seen = 0;
+#pragma unroll
+            for (int w = 0; w < C::kSoftmax / 32; ++w) {
+                if (w < swarp) rank += warp_counts[w];
+                seen += warp_counts[w];
+            }
+            if (mine > 0 && rank < units_per_tile && rank + mine > 0)
+                for (int u = share0; u < share1; ++u)
+                    if (p.idx[u] == h) {
+                        if (rank >= 0 && rank < units_per_tile) unit_list[rank] = u;
+                        ++rank;
+                    }
+            named_barrier(1, C::kSoftmax);
             const int n_units = min(seen - rank0, units_per_tile);
             const int n_rows = n_units * G;
             const bool pair = n_rows > C::kStreamRows;
@@ -438,9 +473,12 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
                         make_int4(slot_id, last - (int)blockIdx.x + 1, i * G, pair ? 0 : 1);
             }
 
-            // the queries, swizzled like a key tile; rows past the tile's are zero
-            for (int i = stid; i < (pair ? 2 : 1) * C::kStreamRows * (D / 8); i += C::kSoftmax) {
-                const int r = i / (D / 8), c = i - r * (D / 8);
+            // the queries, swizzled like a key tile; the last 32 rows are filled up
+            // with zeros, and what lies behind them is nobody's
+            constexpr int kChunks = D / 8, kPass = C::kSoftmax / kChunks;
+            const int c = stid % kChunks;
+#pragma unroll 4
+            for (int r = stid / kChunks; r < ((n_rows + 31) & ~31); r += kPass) {
                 uint4 x = make_uint4(0, 0, 0, 0);
                 if (r < n_rows) {
                     const int e = r / G, u = unit_list[e];
@@ -611,13 +649,14 @@ __global__ void __launch_bounds__(256) sha_prefix_merge_kernel(const PrefixMerge
     const int sub = threadIdx.x % kLanes;
     const long long rows = (long long)p.B * p.top_k * G;
     const long long at = ((long long)blockIdx.x * 256 + threadIdx.x) / kLanes;
-    pdl_wait();
-    pdl_launch_dependents();
+    // (the call's inputs were complete before the passes began)
     const bool inside = at < rows;
     const int u = inside ? (int)(at / G) : 0, j = inside ? (int)(at - (long long)u * G) : 0;
     const int b = u / p.top_k, h = p.idx[u], len = p.seqlens[b];
     // units that no pass has touched
     const bool live = inside && (unsigned)h < (unsigned)p.H_kv && len >= p.min_len && len <= p.max_len;
+    pdl_wait();
+    pdl_launch_dependents();
     int2 run = make_int2(0, 0);
     int4 ref = make_int4(0, 0, 0, 0);
     if (live) {

@@ -115,24 +115,14 @@ struct ClusterWalk {
     }
 };
 
-// Which part of a row's keys a walk covers: keys [key0, len) of a row whose
-// length is in [min_len, n_max], at least one tile of them (a row that ends
-// where its range begins still has a unit to finish).  {1, n_max, 0}: all keys.
-struct KeyRange {
-    int min_len, n_max, key0;
-};
-
-__device__ __forceinline__ int varlen_tiles(int len, const KeyRange &r, int tile)
+__device__ __forceinline__ int varlen_tiles(int len, int n_max, int tile)
 {
-    if (len < r.min_len || len > r.n_max) return 0;
-    const int n = len - r.key0;
-    return n > tile ? (n + tile - 1) / tile : 1;
+    return (len >= 1 && len <= n_max) ? (len + tile - 1) / tile : 0;
 }
 
 struct VarlenWalk {
     const int32_t *seqlens;
-    KeyRange range;
-    int B, top_k, tile;
+    int B, top_k, n_max, tile;
     long long t, t_end;
     int b, k, j, T, n;          // position: row, slot, tile in unit; row's tiles and keys
     long long unit_start;
@@ -148,7 +138,7 @@ struct VarlenWalk {
         s.whole = (j == 0 && run == T);
         s.unit_start = unit_start;
         s.unit_tiles = T;
-        s.n_keys = n - range.key0;
+        s.n_keys = n;
         t += run;
         j += run;
         if (j == T && t < t_end) {        // step to the next unit that has tiles
@@ -159,7 +149,7 @@ struct VarlenWalk {
                 do {
                     ++b;
                     n = seqlens[b];
-                    T = varlen_tiles(n, range, tile);
+                    T = varlen_tiles(n, n_max, tile);
                 } while (T == 0);
             }
         }
@@ -172,7 +162,7 @@ struct VarlenWalk {
 // the block calls it (it synchronises with __syncthreads).  Returns false if
 // this block has nothing to do.  scratch: shared, >= 2 * (NT/32) + 8 longs.
 template <int NT>
-__device__ bool varlen_plan(const int32_t *seqlens, int B, int top_k, KeyRange range, int tile,
+__device__ bool varlen_plan(const int32_t *seqlens, int B, int top_k, int n_max, int tile,
                             int max_blocks, long long *scratch, Schedule &S, VarlenWalk &w)
 {
     constexpr int kWarps = NT / 32;
@@ -184,7 +174,7 @@ __device__ bool varlen_plan(const int32_t *seqlens, int B, int top_k, KeyRange r
     int tmax = 0;
     for (int r = tid; r < B; r += NT) {
         const int len = seqlens[r];
-        const int T = varlen_tiles(len, range, tile);
+        const int T = varlen_tiles(len, n_max, tile);
         if (T == 0 && blockIdx.x == 0) atomicOr(&g_sha_status, kStatusBadIndex);
         sum += (long long)top_k * T;
         tmax = max(tmax, T);
@@ -227,7 +217,7 @@ __device__ bool varlen_plan(const int32_t *seqlens, int B, int top_k, KeyRange r
     for (int r0 = 0; r0 < B; r0 += NT) {
         const int r = r0 + tid;
         const int len = r < B ? seqlens[r] : 0;
-        const int T = r < B ? varlen_tiles(len, range, tile) : 0;
+        const int T = r < B ? varlen_tiles(len, n_max, tile) : 0;
         const long long val = (long long)top_k * T;
         long long incl = val;
 #pragma unroll
@@ -259,7 +249,7 @@ __device__ bool varlen_plan(const int32_t *seqlens, int B, int top_k, KeyRange r
     w.seqlens = seqlens;
     w.B = B;
     w.top_k = top_k;
-    w.range = range;
+    w.n_max = n_max;
     w.tile = tile;
     w.t = t0;
     w.t_end = S.begin(blockIdx.x + 1);
