@@ -863,10 +863,18 @@ sha_status_t decode_impl(const void *q, const void *k, const void *v, const int3
 // prefix and over their own keys, and the two passes' states.
 struct PrefixPlan {
     long long units;
-    int row_tiles_max;           // row tiles the selection can need, at most
     int suffix_slot_floats, prefix_slot_floats;
     size_t runs_at, suffix_at, prefix_at, bytes;   // the references come first
 };
+
+// Row tiles the selection of a call can need: each head's last one may be
+// ragged, the others are full.
+int prefix_tiles_max(int B, int H_q, int H_kv, int top_k)
+{
+    const long long units = (long long)B * top_k;
+    const int per_tile = sha::PrefixConfig<128>::kRows / (H_q / H_kv);
+    return (int)(units / per_tile + (units < H_kv ? units : H_kv));
+}
 
 template <int D>
 PrefixPlan make_prefix_plan(int B, int H_q, int H_kv, int top_k, int num_sms)
@@ -874,10 +882,7 @@ PrefixPlan make_prefix_plan(int B, int H_q, int H_kv, int top_k, int num_sms)
     using C = sha::PrefixConfig<D>;
     PrefixPlan pl;
     const int G = H_q / H_kv;
-    const int per_tile = C::kRows / G;
     pl.units = (long long)B * top_k;
-    // each head's last row tile may be ragged; the others are full
-    pl.row_tiles_max = (int)(pl.units / per_tile + (pl.units < H_kv ? pl.units : H_kv));
     pl.suffix_slot_floats = (G * (D + 2) + 31) / 32 * 32;
     pl.prefix_slot_floats = C::kRows * (D + 2);
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
@@ -887,7 +892,8 @@ PrefixPlan make_prefix_plan(int B, int H_q, int H_kv, int top_k, int num_sms)
                    up((size_t)(pl.units + (long long)num_sms * sha::SuffixConfig<D>::kWorkers) *
                       pl.suffix_slot_floats * sizeof(float));
     pl.bytes = pl.prefix_at +
-               up((size_t)(pl.row_tiles_max + num_sms) * pl.prefix_slot_floats * sizeof(float));
+               up((size_t)(prefix_tiles_max(B, H_q, H_kv, top_k) + num_sms) * pl.prefix_slot_floats *
+                  sizeof(float));
     return pl;
 }
 
@@ -1108,6 +1114,9 @@ sha_status_t sha_decode_prefix(const void *q, const void *k_pages, const void *v
     sha_status_t st = check_prefix_shape(B, H_q, H_kv, d, top_k);
     if (st != SHA_OK) return st;
     if (!boxable_pages(page_size) || (long long)num_pages * H_kv > (1ll << 31) - 1)
+        return SHA_ERR_UNSUPPORTED;
+    // the prefix pass numbers its tiles in 32 bits
+    if ((long long)prefix_tiles_max(B, H_q, H_kv, top_k) * ((prefix_len + 127) / 128) > (1ll << 31) - 1)
         return SHA_ERR_UNSUPPORTED;
     if (B == 0 || top_k == 0) return SHA_OK;
     if (!q || !k_pages || !v_pages || !batch_head_index || !seqlens || !block_table ||

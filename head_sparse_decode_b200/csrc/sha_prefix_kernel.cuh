@@ -156,35 +156,92 @@ __device__ __forceinline__ void prefix_row_tiles(const PrefixParams &p, int unit
     __syncthreads();
 }
 
-// How the row tiles are cut over `blocks` blocks.  Beginning a run (its list, its
-// queries, its state written out) takes a block about as long as kRunTiles key
-// tiles, so whole row tiles, or equal pieces of them, go to the blocks where the
-// busiest then has no more to do than under the even cut, which gives most blocks
-// two runs.  (OPT-66B-shaped, 72 row tiles of 15 key tiles: 2 pieces of 7 or 8
-// each, 144 runs, against 219.)
-constexpr int kRunTiles = 3;
-__device__ __forceinline__ void prefix_cut(Schedule &S, int row_tiles, int blocks)
-{
-    const int tpu = S.tiles_per_unit;
-    S.total_tiles = (long long)row_tiles * tpu;
-    S.pieces = 0;
-    S.num_ctas = S.total_tiles < blocks ? (int)S.total_tiles : blocks;
-    if (row_tiles == 0) return;
-    const long long even = (S.total_tiles + S.num_ctas - 1) / S.num_ctas + 2 * kRunTiles;
-    if (row_tiles <= blocks) {
-        const int p = min(blocks / row_tiles, tpu);
-        if ((tpu + p - 1) / p + kRunTiles <= even) {
-            S.pieces = p;
-            S.num_ctas = row_tiles * p;
+// How the row tiles x key tiles are cut over the blocks: contiguous ranges of the
+// tiles, numbered row-tile-major.  Beginning a run (its list, its queries, its
+// state written out) takes a block about as long as kRunTiles key tiles, so whole
+// row tiles, or equal pieces of them, go to the blocks where the busiest then has
+// no more to do than under the even cut, which gives most blocks two runs.
+// (OPT-66B-shaped, 72 row tiles of 15 key tiles: 2 pieces of 7 or 8 each, 144
+// runs, against 219.)  All in 32 bits -- the host keeps the tiles of a call below
+// 2^31 -- since a 64-bit division costs a lone thread 0.4 us.
+constexpr unsigned kRunTiles = 3;
+
+// A run: tiles [first, first + n) of row tile `row_tile`.
+struct PrefixRun {
+    int row_tile, first, n;
+};
+
+struct PrefixCut {
+    unsigned key_tiles, blocks;
+    unsigned pieces;             // > 0: a row tile is cut into this many, one per block
+    unsigned base, extra;        // else block c has base tiles, the first `extra` one more
+    unsigned t, t_end;           // this block's range
+
+    __device__ __forceinline__ unsigned begin(unsigned c) const
+    {
+        return c * base + min(c, extra);
+    }
+    __device__ __forceinline__ void plan(unsigned row_tiles, unsigned tiles, unsigned grid,
+                                         unsigned block)
+    {
+        key_tiles = tiles;
+        const unsigned total = row_tiles * tiles;
+        blocks = min(total, grid);
+        pieces = 0;
+        base = extra = t = t_end = 0;
+        if (total == 0) return;
+        const unsigned even = (total + blocks - 1) / blocks + 2 * kRunTiles;
+        if (row_tiles <= blocks) {
+            const unsigned p = min(blocks / row_tiles, tiles);
+            if ((tiles + p - 1) / p + kRunTiles <= even) {
+                pieces = p;
+                blocks = row_tiles * p;
+            }
         }
-    } else {
-        const int whole = (row_tiles + blocks - 1) / blocks;
-        if ((long long)whole * (tpu + kRunTiles) <= even) {
-            S.pieces = 1;
-            S.num_ctas = blocks;
+        if (pieces) {
+            if (block < blocks) {
+                const unsigned r = block / pieces, k = block - r * pieces;
+                const unsigned b = tiles / pieces, x = tiles - b * pieces;
+                t = r * tiles + k * b + min(k, x);
+                t_end = t + b + (k < x);
+            }
+            return;
+        }
+        const unsigned whole = (row_tiles + blocks - 1) / blocks;
+        if (row_tiles > blocks && whole * (tiles + kRunTiles) <= even) {
+            t = min(block * whole, row_tiles) * tiles;
+            t_end = min((block + 1) * whole, row_tiles) * tiles;
+            base = whole * tiles;                    // begin() of a block in use
+            return;
+        }
+        base = total / blocks;
+        extra = total - base * blocks;
+        if (block < blocks) {
+            t = begin(block);
+            t_end = begin(block + 1);
         }
     }
-}
+    __device__ __forceinline__ bool next(PrefixRun &r)
+    {
+        if (t >= t_end) return false;
+        r.row_tile = (int)(t / key_tiles);
+        const unsigned end = ((unsigned)r.row_tile + 1) * key_tiles;
+        r.first = (int)(t - (unsigned)r.row_tile * key_tiles);
+        r.n = (int)(min(end, t_end) - t);
+        t += (unsigned)r.n;
+        return true;
+    }
+    // Blocks that share the row tile which this block's run begins.
+    __device__ __forceinline__ int sharers(const PrefixRun &r, unsigned block) const
+    {
+        if (r.first + r.n == (int)key_tiles) return 1;
+        if (pieces) return (int)pieces;
+        const unsigned last = ((unsigned)r.row_tile + 1) * key_tiles - 1;
+        const unsigned split = extra * (base + 1);
+        const unsigned c = last < split ? last / (base + 1) : extra + (last - split) / base;
+        return (int)(c - block) + 1;
+    }
+};
 
 // The head of row tile r: the last h with start[h] <= r among those that have tiles.
 __device__ __forceinline__ int prefix_head_of(const int *start, int H_kv, int r)
@@ -263,19 +320,10 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
     pdl_launch_dependents();
 
     prefix_row_tiles<C::kThreads>(p, units_per_tile, start);
-    const int key_tiles = (p.keys + C::kTile - 1) / C::kTile;
-    Schedule S;
-    S.tiles_per_unit = key_tiles;                    // a "unit" here is a row tile
-    prefix_cut(S, start[p.H_kv], (int)gridDim.x);
-    UniformWalk wk;
-    wk.S = S;
-    wk.t = wk.t_end = 0;
-    if ((int)blockIdx.x < S.num_ctas) {
-        wk.t = S.begin(blockIdx.x);
-        wk.t_end = S.begin(blockIdx.x + 1);
-    }
-    wk.n_keys = p.keys;
-    Seg seg;
+    PrefixCut wk;
+    wk.plan((unsigned)start[p.H_kv], (unsigned)((p.keys + C::kTile - 1) / C::kTile), gridDim.x,
+            blockIdx.x);
+    PrefixRun run;
 
     // waits give up together: the first that runs out raises the abort flag
     auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -295,9 +343,9 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
         long long base = 0;
         bool ok = true;
         const int box_rows = min(p.page_size, C::kTile);
-        while (ok && wk.next(seg)) {
-            const int h = prefix_head_of(start, p.H_kv, (int)seg.unit);
-            const int n = seg.num_tiles;
+        while (ok && wk.next(run)) {
+            const int h = prefix_head_of(start, p.H_kv, run.row_tile);
+            const int n = run.n;
             for (int i = 0; ok && i < 2 * n; ++i) {
                 // position i is K_0, K_((i+1)/2) (odd i < 2n-1) or V
                 const bool is_k = i == 0 || ((i & 1) && i < 2 * n - 1);
@@ -307,7 +355,7 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
                 if (lane == 0) ok = wait(&empty[buf], parity ^ 1);
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
-                const int n0 = (seg.first_tile + jj) * C::kTile;
+                const int n0 = (run.first + jj) * C::kTile;
                 const int rows = min(C::kTile, p.keys - n0);
                 const int chunks = (rows + box_rows - 1) / box_rows;
                 if (lane == 0)
@@ -343,8 +391,8 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
             long long base = 0;
             uint32_t q_parity = 0, p_parity = 0, pv_parity = 0;    // bit per stream
             bool ok = true;
-            while (ok && wk.next(seg)) {
-                const int n = seg.num_tiles;
+            while (ok && wk.next(run)) {
+                const int n = run.n;
                 ok = wait(q_full, q_parity);
                 q_parity ^= 1;
                 if (!ok) break;
@@ -428,8 +476,8 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
         uint32_t s_parity = 0, o_parity = 0;
         long long base = 0;
         bool ok = true;
-        while (wk.next(seg)) {
-            const int rt = (int)seg.unit;
+        while (wk.next(run)) {
+            const int rt = run.row_tile;
             const int h = prefix_head_of(start, p.H_kv, rt);
             // this row tile's units: those of the head's units, in order, that the
             // tiles before it have not taken
@@ -439,8 +487,10 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
             const int per = (units + C::kSoftmax - 1) / C::kSoftmax;
             const int share0 = min(stid * per, units), share1 = min(share0 + per, units);
             int mine = 0;
-#pragma unroll 8
-            for (int u = share0; u < share1; ++u) mine += p.idx[u] == h;
+            for (int u = share0; u < share1; u += 8) {        // eight loads on the way
+#pragma unroll
+                for (int i = 0; i < 8; ++i) mine += u + i < share1 && p.idx[u + i] == h;
+            }
             int incl = mine;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
@@ -466,11 +516,11 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
             const int n_rows = n_units * G;
             const bool pair = n_rows > C::kStreamRows;
             const int slot_id = rt + (int)blockIdx.x;
-            if (seg.first_tile == 0) {
-                const int last = S.cta_of(seg.unit_start + key_tiles - 1);
+            if (run.first == 0) {
+                const int sharers = wk.sharers(run, blockIdx.x);
                 for (int i = stid; i < n_units; i += C::kSoftmax)
                     p.parts.ref[unit_list[i]] =
-                        make_int4(slot_id, last - (int)blockIdx.x + 1, i * G, pair ? 0 : 1);
+                        make_int4(slot_id, sharers, i * G, pair ? 0 : 1);
             }
 
             // the queries, swizzled like a key tile; the last 32 rows are filled up
@@ -501,7 +551,7 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
 
-            const int n = seg.num_tiles;
+            const int n = run.n;
             const int tile_row = (pair ? st * C::kStreamRows : 0) + (swarp & 3) * 32;
             const bool busy = tile_row < n_rows;          // this warp has rows
             float m_ref = -INFINITY, l0 = 0.f, l1 = 0.f;
@@ -509,7 +559,7 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
             for (int i = pair ? 0 : st; i < n; i += pair ? 1 : 2) {
                 if (ok) ok = __all_sync(FULL, wait(&s_full[st], s_parity));
                 s_parity ^= 1;
-                const int rows = min(C::kTile, p.keys - (seg.first_tile + i) * C::kTile);
+                const int rows = min(C::kTile, p.keys - (run.first + i) * C::kTile);
                 if (rows < C::kTile) {
                     // rows past the prefix hold other keys or nothing: zero V there
                     // (0 * NaN) before any product with this tile's P.  Both streams

@@ -80,6 +80,13 @@ __device__ __forceinline__ int suffix_stages(const SuffixParams &p, int len, int
     return n > stage ? (n + stage - 1) / stage : 1;
 }
 
+// a / b, in 32 bits where both fit (a 64-bit division costs a lone warp 0.4 us).
+__device__ __forceinline__ long long div_small(long long a, long long b)
+{
+    if (((a | b) >> 32) == 0) return (unsigned)a / (unsigned)b;
+    return a / b;
+}
+
 struct SuffixRun {
     int unit, b;
     int first, n;        // stages of the unit
@@ -89,16 +96,22 @@ struct SuffixRun {
 
 // A worker's range of the units' weights, walked unit by unit.
 struct SuffixWalk {
-    long long total, t, t_end;
+    long long base, t, t_end;          // workers have base weights, the first `extra` one more
     long long unit_start;
-    int workers;
+    int extra;
     int b, k, T, len;                  // current unit: row, slot, stages, row length
 
-    __device__ __forceinline__ long long begin(int w) const { return w * total / workers; }
+    __device__ __forceinline__ long long begin(int w) const
+    {
+        return w * base + (w < extra ? w : extra);
+    }
     // the last worker of the unit that this worker's run `r` begins
     __device__ __forceinline__ int last_worker(const SuffixRun &r, int worker) const
     {
-        return r.end <= t_end ? worker : (int)((r.end * workers - 1) / total);
+        if (r.end <= t_end) return worker;
+        const long long last = r.end - 1, split = (long long)extra * (base + 1);
+        return last < split ? (int)div_small(last, base + 1)
+                            : extra + (int)div_small(last - split, base);
     }
     template <int D>
     __device__ __forceinline__ bool next(const SuffixParams &p, SuffixRun &r)
@@ -163,22 +176,22 @@ __device__ __forceinline__ bool suffix_plan(const SuffixParams &p, long long *sc
         scratch[2 * warp + 1] = tmax;
     }
     __syncthreads();
-    w.total = 0;
+    long long total = 0;
     tmax = 0;
     for (int i = 0; i < C::kWorkers; ++i) {
-        w.total += scratch[2 * i];
+        total += scratch[2 * i];
         tmax = max(tmax, (int)scratch[2 * i + 1]);
     }
-    if (w.total == 0) return false;
+    if (total == 0) return false;
     // workers in use: each with kMinWeight at least, and no unit in many more than
     // kMaxRuns pieces
     long long least = (tmax + C::kMaxRuns - 1) / C::kMaxRuns;
     if (least < C::kMinWeight) least = C::kMinWeight;
-    long long n = w.total / least;
-    const long long all = (long long)gridDim.x * C::kWorkers;
-    n = n < 1 ? 1 : n > all ? all : n;
-    w.workers = (int)n;
-    if (worker >= w.workers) return false;
+    const int all = (int)gridDim.x * C::kWorkers;
+    const int n = total >= all * least ? all : total < least ? 1 : (int)div_small(total, least);
+    if (worker >= n) return false;
+    w.base = div_small(total, n);
+    w.extra = (int)(total - w.base * n);
     w.t = w.begin(worker);
     w.t_end = w.begin(worker + 1);
 
@@ -204,7 +217,7 @@ __device__ __forceinline__ bool suffix_plan(const SuffixParams &p, long long *sc
             w.T = __shfl_sync(FULL, T, src);
             w.len = __shfl_sync(FULL, len, src);
             const long long start = __shfl_sync(FULL, row_start, src);
-            w.k = (int)((w.t - start) / (w.T + C::kUnitCost));
+            w.k = (int)div_small(w.t - start, w.T + C::kUnitCost);
             w.unit_start = start + (long long)w.k * (w.T + C::kUnitCost);
             return true;
         }

@@ -207,7 +207,8 @@ sha_status_t sha_decode_paged(const void *q, const void *k_pages, const void *v_
  *                  row b attends to keys [0, seqlens[b]); of its block_table only
  *                  the entries from prefix_len / page_size on are read
  *   page_size    : a power of two >= 8, for every G (SHA_ERR_UNSUPPORTED otherwise);
- *                  H_kv <= 1024, B * top_k <= 2^24
+ *                  H_kv <= 1024, B * top_k <= 2^24, and ceil(prefix_len / 128) times
+ *                  (B * top_k * G / 256 + H_kv) below 2^31
  *   workspace    : device, 256-byte aligned, >= sha_decode_prefix_workspace_size
  *                  bytes; scratch only (no contents carried between calls), owned
  *                  by the caller; calls that share it must not overlap on the device
