@@ -16,6 +16,7 @@ batch_head_index [B, top_k] int32 on the same device.  Rows of out whose head
 is not selected are left exactly as they were.
 """
 import ctypes
+import functools
 import math
 import os
 
@@ -265,10 +266,16 @@ _lib.sha_decode_prefix_workspace_size.argtypes = [_i] * 5
 _lib.sha_decode_prefix_workspace_size.restype = ctypes.c_size_t
 
 
+@functools.lru_cache(maxsize=1024)
+def _prefix_workspace_size(B, H_q, H_kv, d, top_k, index):
+    with torch.cuda.device(index):
+        return int(_lib.sha_decode_prefix_workspace_size(B, H_q, H_kv, d, top_k))
+
+
 def sha_decode_prefix_workspace_size(B, H_q, H_kv, d, top_k, device=None):
     """Workspace bytes sha_decode_prefix needs for these sizes on ``device``."""
     with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
-        return int(_lib.sha_decode_prefix_workspace_size(B, H_q, H_kv, d, top_k))
+        return _prefix_workspace_size(B, H_q, H_kv, d, top_k, torch.cuda.current_device())
 
 
 def sha_decode_prefix(q, k_pages, v_pages, batch_head_index, seqlens, block_table, prefix_len,
@@ -283,8 +290,8 @@ def sha_decode_prefix(q, k_pages, v_pages, batch_head_index, seqlens, block_tabl
     if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
         raise ValueError("k_pages and v_pages must both be [num_pages, H_kv, page_size, d]")
     num_pages, H_kv, page_size, d = k_pages.shape
-    dev, dtype = k_pages.device, k_pages.dtype
-    if not k_pages.is_cuda:
+    dev, dtype, index = k_pages.device, k_pages.dtype, k_pages.get_device()
+    if index < 0:
         raise ValueError("k_pages must be a CUDA tensor")
     if q.dim() == 4 and q.shape[2] != 1:
         raise ValueError("decode takes one query token: q must be [B, H_q, 1, d]")
@@ -304,29 +311,30 @@ def sha_decode_prefix(q, k_pages, v_pages, batch_head_index, seqlens, block_tabl
         raise ValueError("prefix_table must hold ceil(prefix_len / page_size) page ids")
     if seqlens.shape != (B,):
         raise ValueError("seqlens must be [B]")
-    for name, t, dt in (("q", q, dtype), ("k_pages", k_pages, dtype), ("v_pages", v_pages, dtype),
-                        ("out", out, dtype), ("batch_head_index", batch_head_index, torch.int32),
-                        ("seqlens", seqlens, torch.int32), ("block_table", block_table, torch.int32),
-                        ("prefix_table", prefix_table, torch.int32)):
-        if t.dtype != dt or not t.is_contiguous() or t.device != dev:
-            raise ValueError(f"{name} must be a contiguous {dt} tensor on {dev}")
+    _check_contiguous("q", q, q.dim(), dtype, index)
+    _check_contiguous("k_pages", k_pages, 4, dtype, index)
+    _check_contiguous("v_pages", v_pages, 4, dtype, index)
+    _check_contiguous("out", out, out.dim(), dtype, index)
+    _check_contiguous("batch_head_index", batch_head_index, 2, torch.int32, index)
+    _check_contiguous("seqlens", seqlens, 1, torch.int32, index)
+    _check_contiguous("block_table", block_table, 2, torch.int32, index)
+    _check_contiguous("prefix_table", prefix_table, 1, torch.int32, index)
     top_k = batch_head_index.shape[1]
     code = _dtype_code(dtype)
-    handle = _stream_handle(stream, dev)
-    with torch.cuda.device(dev):
-        if workspace is None:
-            nbytes = _lib.sha_decode_prefix_workspace_size(B, H_q, H_kv, d, top_k)
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-            if handle != torch.cuda.current_stream(dev).cuda_stream:
-                workspace.record_stream(torch.cuda.ExternalStream(handle, device=dev))
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-        _check(_lib.sha_decode_prefix(
-            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), batch_head_index.data_ptr(),
-            seqlens.data_ptr(), block_table.data_ptr(), prefix_table.data_ptr(), prefix_len, B, H_q,
-            H_kv, num_pages, page_size, block_table.shape[1], d, top_k, _default_scale(scale, d),
-            out.data_ptr(), code, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), handle))
+    handle = _raw_stream(stream, dev)
+    if workspace is None:
+        nbytes = _prefix_workspace_size(B, H_q, H_kv, d, top_k, index)
+        workspace = seqlens.new_empty((nbytes + 3) // 4)
+        if stream is not None and handle != torch._C._cuda_getCurrentRawStream(index):
+            workspace.record_stream(torch.cuda.ExternalStream(handle, device=dev))
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    _on_device(dev, _lib.sha_decode_prefix,
+               (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), batch_head_index.data_ptr(),
+                seqlens.data_ptr(), block_table.data_ptr(), prefix_table.data_ptr(), prefix_len, B,
+                H_q, H_kv, num_pages, page_size, block_table.shape[1], d, top_k,
+                _default_scale(scale, d), out.data_ptr(), code, workspace.data_ptr(),
+                workspace.numel() * workspace.element_size(), handle))
     return out
 
 
@@ -591,38 +599,54 @@ _lib.sha_append_paged.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp,
 _lib.sha_append_paged.restype = _i
 
 
-def _on_device(device, entry, *args, stream=None):
-    """entry(*args, stream) with `device` current; raises on an error status.  The
-    device is switched only if it is not the current one already."""
-    handle = _stream_handle(stream, device)
+def _raw_stream(stream, device):
+    """_stream_handle without the cost of a torch.cuda.Stream object for the current stream."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return _stream_handle(stream, device)
+
+
+def _on_device(device, entry, args):
+    """entry(*args) with `device` current; raises on an error status.  The device is
+    switched only if it is not the current one already."""
     if device.index == torch.cuda.current_device():
-        _check(entry(*args, handle))
+        status = entry(*args)
     else:
         with torch.cuda.device(device):
-            _check(entry(*args, handle))
+            status = entry(*args)
+    if status != SHA_OK:
+        raise ShaError(status)
 
 
-def _check_heads_view(name, t, like=None):
-    """A [T, H, d] CUDA view with d contiguous, of `like`'s dtype and device."""
-    if t.dim() != 3 or not t.is_cuda or (t.stride(2) != 1 and t.shape[2] > 1):
-        raise ValueError(f"{name} must be a CUDA tensor [T, H, d] with d contiguous")
-    if like is not None:
-        if t.device != like.device:
-            raise ValueError(f"{name} is on {t.device}, expected {like.device}")
-        if t.dtype != like.dtype:
-            raise TypeError(f"{name} has dtype {t.dtype}, expected {like.dtype}")
+@functools.lru_cache(maxsize=1024)
+def _stride_pair(s0, s1):
+    return _i64x2(s0, s1)
 
 
-def _check_vector(name, t, length, dtype, device):
-    if t.dim() != 1 or t.shape[0] != length or t.dtype != dtype or not t.is_contiguous() \
-            or t.device != device:
-        raise ValueError(f"{name} must be a contiguous {dtype} [{length}] tensor on {device}")
+def _check_heads_view(name, t, dtype, index):
+    """A [T, H, d] view with d contiguous, of `dtype`, on CUDA device `index`; its strides."""
+    if t.dim() != 3 or index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor [T, H, d]")
+    strides = t.stride()
+    if strides[2] != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name} must have d contiguous")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    return _stride_pair(strides[0], strides[1])
 
 
-def _check_inv_freq(inv_freq, device):
-    if inv_freq.dim() != 1 or inv_freq.dtype != torch.float64 or not inv_freq.is_contiguous() \
-            or inv_freq.device != device:
-        raise ValueError(f"inv_freq must be a contiguous float64 [rotary/2] tensor on {device}")
+def _check_contiguous(name, t, dims, dtype, index):
+    if t.dim() != dims or t.dtype != dtype or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {dims} dimensions "
+                         f"on cuda:{index}")
+
+
+def _check_vector(name, t, length, index):
+    _check_contiguous(name, t, 1, torch.int32, index)
+    if t.shape[0] != length:
+        raise ValueError(f"{name} must hold {length} entries")
 
 
 def rope_frequencies(rotary, base=10000.0, scaling=None, device=None):
@@ -698,21 +722,20 @@ def sha_rope(x, positions, inv_freq, out=None, interleaved=False, mscale=1.0, st
     positions int32 [T], inv_freq float64 [rotary/2] (rope_frequencies), all on one
     device.  out (default: a new contiguous tensor) may be x itself.  Rotating by
     -positions is the inverse up to mscale^2, and the gradient."""
-    _check_heads_view("x", x)
-    dev = x.device
+    index, dtype = x.get_device(), x.dtype
+    xs = _check_heads_view("x", x, dtype, index)
     T, H, d = x.shape
-    _check_vector("positions", positions, T, torch.int32, dev)
-    _check_inv_freq(inv_freq, dev)
+    _check_vector("positions", positions, T, index)
+    _check_contiguous("inv_freq", inv_freq, 1, torch.float64, index)
     if out is None:
-        out = torch.empty((T, H, d), dtype=x.dtype, device=dev)
-    else:
-        _check_heads_view("out", out, x)
-        if out.shape != x.shape:
-            raise ValueError("out must have x's shape")
-    _on_device(dev, _lib.sha_rope, x.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), T, H, d,
-               2 * inv_freq.shape[0], 1 if interleaved else 0, mscale,
-               _i64x2(x.stride(0), x.stride(1)), out.data_ptr(),
-               _i64x2(out.stride(0), out.stride(1)), _dtype_code(x.dtype), stream=stream)
+        out = x.new_empty((T, H, d))
+    elif out.shape != x.shape:
+        raise ValueError("out must have x's shape")
+    os_ = _check_heads_view("out", out, dtype, index)
+    _on_device(x.device, _lib.sha_rope,
+               (x.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), T, H, d,
+                2 * inv_freq.shape[0], 1 if interleaved else 0, mscale, xs, out.data_ptr(), os_,
+                _dtype_code(dtype), _raw_stream(stream, x.device)))
     return out
 
 
@@ -725,52 +748,48 @@ def sha_append_paged(k, v, k_pages, v_pages, block_table, positions, rows=None, 
     inv_freq (float64 [rotary/2]) keys turn by their position on the way, and q
     [T, H_q, d] turns into q_out (default: a new tensor; may be q itself).  Returns
     q_out (None without q)."""
-    _check_heads_view("k", k)
-    _check_heads_view("v", v, k)
+    index, dtype = k.get_device(), k.dtype
+    ks = _check_heads_view("k", k, dtype, index)
+    vs = _check_heads_view("v", v, dtype, index)
     T, H_kv, d = k.shape
     if v.shape != k.shape:
         raise ValueError("v must have k's shape")
-    dev = k.device
-    if k_pages.dim() != 4 or k_pages.shape[1] != H_kv or k_pages.shape[3] != d \
-            or v_pages.shape != k_pages.shape:
+    _check_contiguous("k_pages", k_pages, 4, dtype, index)
+    _check_contiguous("v_pages", v_pages, 4, dtype, index)
+    num_pages, page_heads, page_size, page_d = k_pages.shape
+    if page_heads != H_kv or page_d != d or v_pages.shape != k_pages.shape:
         raise ValueError("k_pages and v_pages must both be [num_pages, H_kv, page_size, d]")
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if t.dtype != k.dtype or t.device != dev or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {k.dtype} tensor on {dev}")
-    if block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.device != dev \
-            or not block_table.is_contiguous():
-        raise ValueError(f"block_table must be a contiguous int32 [B, max_pages] tensor on {dev}")
-    _check_vector("positions", positions, T, torch.int32, dev)
+    _check_contiguous("block_table", block_table, 2, torch.int32, index)
+    _check_vector("positions", positions, T, index)
+    rp, rotary, freq = None, 0, None
     if rows is not None:
-        _check_vector("rows", rows, T, torch.int32, dev)
-    rotary, freq = 0, None
+        _check_vector("rows", rows, T, index)
+        rp = rows.data_ptr()
     if inv_freq is not None:
-        _check_inv_freq(inv_freq, dev)
+        _check_contiguous("inv_freq", inv_freq, 1, torch.float64, index)
         rotary, freq = 2 * inv_freq.shape[0], inv_freq.data_ptr()
     H_q, qp, qs, op, os_ = 0, None, None, None, None
     if q is not None:
         if inv_freq is None:
             raise ValueError("q needs inv_freq: without a rotation there is nothing to do to it")
-        _check_heads_view("q", q, k)
-        if q.shape[0] != T or q.shape[2] != d:
+        qs = _check_heads_view("q", q, dtype, index)
+        shape = q.shape
+        if shape[0] != T or shape[2] != d:
             raise ValueError("q must be [T, H_q, d]")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        else:
-            _check_heads_view("q_out", q_out, k)
-            if q_out.shape != q.shape:
-                raise ValueError("q_out must have q's shape")
-        H_q, qp, op = q.shape[1], q.data_ptr(), q_out.data_ptr()
-        qs, os_ = _i64x2(q.stride(0), q.stride(1)), _i64x2(q_out.stride(0), q_out.stride(1))
+            q_out = q.new_empty(shape)
+        elif q_out.shape != shape:
+            raise ValueError("q_out must have q's shape")
+        os_ = _check_heads_view("q_out", q_out, dtype, index)
+        H_q, qp, op = shape[1], q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _on_device(dev, _lib.sha_append_paged, k.data_ptr(), v.data_ptr(),
-               _i64x2(k.stride(0), k.stride(1)), _i64x2(v.stride(0), v.stride(1)), T, H_kv, d,
-               k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
-               None if rows is None else rows.data_ptr(), positions.data_ptr(),
-               block_table.shape[0], k_pages.shape[0], k_pages.shape[2], block_table.shape[1], freq,
-               rotary, 1 if interleaved else 0, mscale, qp, qs, H_q, op, os_,
-               _dtype_code(k.dtype), stream=stream)
+    B, max_pages = block_table.shape
+    _on_device(k.device, _lib.sha_append_paged,
+               (k.data_ptr(), v.data_ptr(), ks, vs, T, H_kv, d, k_pages.data_ptr(),
+                v_pages.data_ptr(), block_table.data_ptr(), rp, positions.data_ptr(), B, num_pages,
+                page_size, max_pages, freq, rotary, 1 if interleaved else 0, mscale, qp, qs, H_q, op,
+                os_, _dtype_code(dtype), _raw_stream(stream, k.device)))
     return q_out
 
 
