@@ -21,24 +21,30 @@
 // ... : run (row tile r, block c) has slot r + c, since every next run advances
 // one of the two or both.
 //
-// How a tile is computed.  Two streams of 128 query rows share the tensor cores:
+// How a tile is computed.  Two streams of 128 query rows share the tensor cores, in
+// steps of 64 keys:
 //   * a producer warp brings the K and V tiles into a ring with TMA, in the order
 //     in which they are used;
-//   * one thread issues the products: S = Q K^T (both operands in shared memory)
-//     into 128 columns of tensor memory per stream, O += P V (P from tensor memory,
-//     V as it lies, MN-major) into d more;
-//   * each stream's four softmax warps own one query row per thread: they read S,
-//     write P = 2^(S c - m) over it, 16 bits wide (the type of the operands; the
-//     sums l stay fp32 and add the unrounded P), and sum l.  A row's reference m
-//     moves only when a tile's maximum exceeds it by more than 2^8: the weights
-//     then stay below 256, any m is exact, and the accumulator in tensor memory is
-//     rescaled in a few tiles instead of in all.
-// While one stream's warps work on their scores the other stream's products run.
-// A row tile of more than 128 rows gives each stream 128 of them and the same key
-// tiles (compute-bound: the exponentials, 16 a clock, and the products, 2 x 512
-// clocks a tile and stream, are about level); one of up to 128 rows gives both
-// streams the same rows and every other key tile each (memory-bound: two key tiles
-// in flight hide the chain S -> softmax -> P V of each).
+//   * one warp per stream issues its products: S = Q K^T (both operands in shared
+//     memory) into 64 columns of tensor memory, O += P V (P from 32 columns of
+//     tensor memory, V as it lies, MN-major) into d more.  (A lone warp takes about
+//     500 clocks to wait for and issue a product: one for both streams was the
+//     bound, 7500 clocks a tile of 256 rows by 128 keys.)
+//   * each stream's four softmax warps own one query row per thread: they read S
+//     into registers, which frees it for the next step's product at once, and write
+//     P = 2^(S c - m), 16 bits wide (the type of the operands; the sums l stay fp32
+//     and add the unrounded P).  A row's reference m moves only when a step's
+//     maximum exceeds it by more than 2^8: the weights then stay below 256, any m is
+//     exact, and the accumulator in tensor memory is rescaled in a few steps instead
+//     of in all.
+// So a step's exponentials run beside the next step's S and the last one's P V.
+// (Steps of 128 keys leave P no columns of its own but S's: each product then waits
+// for the one before it and the exponentials for both, 4840 clocks for a tile of 256
+// rows by 128 keys against %%.)
+// A row tile of more than 128 rows gives each stream 128 of them and every key of a
+// tile (bound by the exponentials, 16 a clock, and the products, about level); one
+// of up to 128 rows gives both streams the same rows and one half of each key tile
+// (bound by memory).
 #pragma once
 
 #include <cuda.h>
@@ -90,7 +96,7 @@ struct PrefixMergeParams {
 template <int D>
 struct PrefixConfig {
     using Tile = GqaConfig<D>;                       // key tiles and their swizzle
-    static constexpr int kThreads = 384;             // producer, MMA, 2 spare warps; 2 x 4 softmax warps
+    static constexpr int kThreads = 384;             // producer, 2 MMA, 1 spare warp; 2 x 4 softmax warps
     static constexpr int kSoftmax = 256;
     static constexpr int kSoftmaxWarp = 4;           // the first one
     static constexpr int kStreamRows = 128;
@@ -101,18 +107,21 @@ struct PrefixConfig {
     static constexpr int kQOffset = kBufs * kTileBytes;
     static constexpr int kQBytes = kTileBytes;       // 128 query rows, laid out like a key tile
     static constexpr int kBarOffset = kQOffset + 2 * kQBytes;
-    static constexpr int kBars = 2 * kBufs + 1 + 2 + 2 + 2 + 2 + 1;
+    static constexpr int kStep = 64;                 // keys of a step
+    static constexpr int kBars = 2 * kBufs + 2 + 2 + 2 + 2 + 2 + 2;
     static constexpr int kCtlOffset = kBarOffset + 8 * kBars + 8;   // abort, mode, TMEM base
     static constexpr int kWarpOffset = kCtlOffset + 16;             // warp counts of the list
     static constexpr int kUnitOffset = kWarpOffset + 4 * 8;         // a row tile's units
-    static constexpr int kStartOffset = kUnitOffset + 4 * kRows;    // first row tile of each head
+    static constexpr int kQRowOffset = kUnitOffset + 4 * kRows;     // and the rows of q they are
+    static constexpr int kStartOffset = kQRowOffset + 4 * kRows;    // first row tile of each head
     static constexpr int kSmemBytes = 1024 + kStartOffset + 4 * (kPrefixMaxHeads + 1);
-    // tensor memory: S (and P) of the two streams, then O
+    // tensor memory: S of the two streams, P, then O
     static constexpr int kTmemCols = 512;
+    static constexpr int kTmemP = 2 * kStep;
     static constexpr int kTmemO = 256;
-    static_assert(kTile == 128, "128 keys: the N of S, the K of P V");
+    static_assert(kTile == 2 * kStep, "two steps of a tile, one per stream or two of both");
     static_assert(kBarOffset % 8 == 0 && kCtlOffset % 4 == 0, "alignment");
-    static_assert(kTmemO + 2 * D <= kTmemCols, "S and O of both streams fit");
+    static_assert(kTmemP + kStep <= kTmemO && kTmemO + 2 * D <= kTmemCols, "S, P and O fit");
 };
 
 // A row's reference m moves when a tile's maximum exceeds it by more than this
@@ -260,6 +269,32 @@ __device__ __forceinline__ int prefix_head_of(const int *start, int H_kv, int r)
 __device__ __forceinline__ int prefix_k_pos(int i) { return i == 0 ? 0 : 2 * i - 1; }
 __device__ __forceinline__ int prefix_v_pos(int i, int n) { return i < n - 1 ? 2 * i + 2 : 2 * n - 1; }
 
+// The steps of 64 keys that the two streams take through a run of `tiles` key
+// tiles, the last with `rows` keys: paired streams take both halves of every tile,
+// others one each.  Stream 1 never takes more than stream 0.
+struct PrefixSteps {
+    bool pair;
+    int tiles, last_halves;          // halves of the last tile that hold keys: 1 or 2
+
+    __device__ __forceinline__ PrefixSteps(bool pair_, int tiles_, int rows)
+        : pair(pair_), tiles(tiles_), last_halves(rows > 64 ? 2 : 1)
+    {
+    }
+    __device__ __forceinline__ int count(int st) const
+    {
+        return pair ? 2 * tiles - 2 + last_halves : st < last_halves ? tiles : tiles - 1;
+    }
+    __device__ __forceinline__ int tile(int step) const { return pair ? step >> 1 : step; }
+    __device__ __forceinline__ int half(int st, int step) const { return pair ? step & 1 : st; }
+    // whether no later step of the stream needs this step's tile
+    __device__ __forceinline__ bool last_of_tile(int st, int step) const
+    {
+        return !pair || (step & 1) || step == count(st) - 1;
+    }
+    // whether the stream has a step in the last tile
+    __device__ __forceinline__ bool takes_last(int st) const { return pair || st < last_halves; }
+};
+
 template <typename T, int D>
 __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
     sha_prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_k,
@@ -268,7 +303,7 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
     using C = PrefixConfig<D>;
     using Tile = typename C::Tile;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-    constexpr uint32_t kIdescS = umma_idesc_f16(kBf16, 128, C::kTile);
+    constexpr uint32_t kIdescS = umma_idesc_f16(kBf16, 128, C::kStep);
     constexpr uint32_t kIdescO = umma_idesc_f16(kBf16, 128, D, false, true);
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>(
@@ -276,15 +311,17 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBarOffset);
     uint64_t *empty = full + C::kBufs;
     uint64_t *q_full = empty + C::kBufs;       // a run's queries are in shared memory
-    uint64_t *s_full = q_full + 1;             // [stream] S is in tensor memory
-    uint64_t *p_full = s_full + 2;             // [stream] P is
-    uint64_t *pv_done = p_full + 2;            // [stream] P V has read P
-    uint64_t *o_done = pv_done + 2;            // [stream] the run's last P V is done
-    uint64_t *drain = o_done + 2;
+    uint64_t *q_seen = q_full + 1;             // both streams' MMA warps have begun the run
+    uint64_t *s_full = q_seen + 1;             // [stream] S is in tensor memory
+    uint64_t *s_free = s_full + 2;             // [stream] S has been read
+    uint64_t *p_full = s_free + 2;             // [stream] P is in tensor memory
+    uint64_t *pv_done = p_full + 2;            // [stream] P V is done: P read, O up to date
+    uint64_t *drain = pv_done + 2;             // [stream] before tensor memory is freed
     volatile int *ctl = reinterpret_cast<volatile int *>(smem + C::kCtlOffset);
     volatile int *abort_flag = ctl, *paired = ctl + 1;
     int *warp_counts = reinterpret_cast<int *>(smem + C::kWarpOffset);
     int *unit_list = reinterpret_cast<int *>(smem + C::kUnitOffset);
+    int *q_rows = reinterpret_cast<int *>(smem + C::kQRowOffset);
     int *start = reinterpret_cast<int *>(smem + C::kStartOffset);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
@@ -295,16 +332,17 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
     if (tid == 0) {
         for (int s = 0; s < C::kBufs; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&empty[s], 2);                 // both streams have used the tile
         }
         mbar_init(q_full, C::kSoftmax / 32);
+        mbar_init(q_seen, 2);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&s_full[s], 1);
+            mbar_init(&s_free[s], 4);
             mbar_init(&p_full[s], 4);
             mbar_init(&pv_done[s], 1);
-            mbar_init(&o_done[s], 1);
+            mbar_init(&drain[s], 1);
         }
-        mbar_init(drain, 1);
         *abort_flag = 0;
         mbar_init_fence();
     }
@@ -327,20 +365,23 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
 
     // waits give up together: the first that runs out raises the abort flag
     auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (mbar_try_wait(bar, parity)) return true;
         if (*abort_flag) return false;
         if (mbar_wait(bar, parity)) return true;
         atomicOr(&g_sha_status, kStatusTimeout);
         *abort_flag = 1;
         return false;
     };
-
+    auto wait_warp = [&](uint64_t *bar, uint32_t parity) {      // by a whole warp, agreed
+        return (bool)__all_sync(0xffffffffu, wait(bar, parity));
+    };
     if (warp == 0) {
         // -------------------------------------------------------- producer
         // every call reads the prefix again: the L2's default policy may keep it
         uint64_t policy;
         asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
         uint32_t used = 0, last_parity = 0;
-        long long base = 0;
+        uint32_t base = 0;
         bool ok = true;
         const int box_rows = min(p.page_size, C::kTile);
         while (ok && wk.next(run)) {
@@ -350,8 +391,8 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
                 // position i is K_0, K_((i+1)/2) (odd i < 2n-1) or V
                 const bool is_k = i == 0 || ((i & 1) && i < 2 * n - 1);
                 const int jj = is_k ? (i + 1) / 2 : (i == 2 * n - 1 ? n - 1 : i / 2 - 1);
-                const int buf = (int)((base + i) % C::kBufs);
-                const uint32_t parity = (uint32_t)((base + i) / C::kBufs) & 1u;
+                const int buf = (int)((base + (uint32_t)i) % C::kBufs);
+                const uint32_t parity = ((base + (uint32_t)i) / C::kBufs) & 1u;
                 if (lane == 0) ok = wait(&empty[buf], parity ^ 1);
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
@@ -385,81 +426,84 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
             for (int s = 0; s < C::kBufs; ++s)
                 if (used & (1u << s)) mbar_wait_drain(&full[s], (last_parity >> s) & 1u);
         __syncwarp();
-    } else if (warp == 1) {
+    } else if (warp <= 2) {
         // -------------------------------------------------------- products
-        if (lane == 0) {
-            long long base = 0;
-            uint32_t q_parity = 0, p_parity = 0, pv_parity = 0;    // bit per stream
-            bool ok = true;
-            while (ok && wk.next(run)) {
-                const int n = run.n;
-                ok = wait(q_full, q_parity);
-                q_parity ^= 1;
+        // (the whole warp runs this, and one lane of it issues: see elect_one)
+        const int st = warp - 1;
+        const uint32_t leader = elect_one();
+        uint32_t base = 0, q_parity = 0, s_parity = 0, p_parity = 0;
+        // a descriptor's address field counts 16-byte units: tiles and k-steps add to
+        // the whole
+        const uint64_t q_desc = umma_desc_k_sw128(smem_addr(smem + C::kQOffset));
+        const uint64_t k_desc = umma_desc_k_sw128(smem_addr(smem));
+        const uint64_t v_desc = umma_desc_mn_sw128(smem_addr(smem), Tile::kBoxBytes, 1024);
+        constexpr uint32_t kHalf = C::kStep * 128 >> 4;            // 64 key rows of a box
+        const uint32_t s_at = tmem + st * C::kStep, o_at = tmem + C::kTmemO + st * D;
+        const uint32_t p_at = tmem + C::kTmemP + st * (C::kStep / 2);
+        bool ok = true;
+        while (ok && wk.next(run)) {
+            const int n = run.n;
+            ok = wait_warp(q_full, q_parity);
+            q_parity ^= 1;
+            if (!ok) break;
+            tc_fence_after_sync();
+            const bool pair = __any_sync(0xffffffffu, *paired != 0);
+            if (lane == 0) mbar_arrive(q_seen);
+            const PrefixSteps steps(pair, n, p.keys - (run.first + n - 1) * C::kTile);
+            const int count = steps.count(st);
+            const uint64_t qd = q_desc + (pair ? st : 0) * (C::kQBytes >> 4);
+            // S of a step; this stream's last one of a tile gives up its K
+            auto scores = [&](int step) {
+                const uint32_t pos = base + prefix_k_pos(steps.tile(step));
+                const uint32_t buf = pos % C::kBufs;
+                if (!wait_warp(&full[buf], (pos / C::kBufs) & 1u)) return false;
+                const uint64_t kd = k_desc + buf * (C::kTileBytes >> 4) +
+                                    (uint32_t)steps.half(st, step) * kHalf;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    constexpr int kBox = Tile::kBoxBytes >> 4;
+                    umma_f16_elected(leader, s_at, qd + (ks >> 2) * kBox + (ks & 3) * 2,
+                                     kd + (ks >> 2) * kBox + (ks & 3) * 2, kIdescS, ks > 0);
+                }
+                umma_commit_elected(leader, &s_full[st]);
+                if (steps.last_of_tile(st, step)) umma_commit_elected(leader, &empty[buf]);
+                return true;
+            };
+            if (count > 0) ok = scores(0);
+            for (int step = 0; ok && step < count; ++step) {
+                // S has been read: the next step's may take its place
+                if (step + 1 < count) {
+                    ok = wait_warp(&s_free[st], s_parity);
+                    tc_fence_after_sync();
+                    ok = ok && scores(step + 1);
+                }
+                s_parity ^= 1;
+                // O += P V; this stream's last one of a tile gives up its V
+                const uint32_t pos = base + prefix_v_pos(steps.tile(step), n);
+                const uint32_t buf = pos % C::kBufs;
+                ok = ok && wait_warp(&full[buf], (pos / C::kBufs) & 1u);
+                ok = ok && wait_warp(&p_full[st], p_parity);
+                p_parity ^= 1;
                 if (!ok) break;
                 tc_fence_after_sync();
-                const bool pair = *paired != 0;
-                // S of tile i for a stream; `last`: no other stream reads this K tile after it
-                auto scores = [&](int st, int i, bool last) {
-                    const long long pos = base + prefix_k_pos(i);
-                    const int buf = (int)(pos % C::kBufs);
-                    if (!wait(&full[buf], (uint32_t)(pos / C::kBufs) & 1u)) return false;
-                    const uint32_t qa = smem_addr(smem + C::kQOffset + (pair ? st : 0) * C::kQBytes);
-                    const uint32_t kb = smem_addr(smem + buf * C::kTileBytes);
+                const uint64_t vd = v_desc + buf * (C::kTileBytes >> 4) +
+                                    (uint32_t)steps.half(st, step) * kHalf;
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint32_t at = (ks >> 2) * Tile::kBoxBytes + (ks & 3) * 32;
-                        umma_f16(tmem + st * 128, umma_desc_k_sw128(qa + at),
-                                 umma_desc_k_sw128(kb + at), kIdescS, ks > 0);
-                    }
-                    umma_commit(&s_full[st]);
-                    if (last) umma_commit(&empty[buf]);
-                    return true;
-                };
-                // O += P V of tile i; then S of tile `next` may take P's place
-                auto outputs = [&](int st, int i, bool first, bool last, bool end) {
-                    if (!wait(&p_full[st], (p_parity >> st) & 1u)) return false;
-                    p_parity ^= 1u << st;
-                    const long long pos = base + prefix_v_pos(i, n);
-                    const int buf = (int)(pos % C::kBufs);
-                    if (!wait(&full[buf], (uint32_t)(pos / C::kBufs) & 1u)) return false;
-                    tc_fence_after_sync();
-                    const uint32_t vb = smem_addr(smem + buf * C::kTileBytes);
-#pragma unroll
-                    for (int ks = 0; ks < C::kTile / 16; ++ks)
-                        umma_f16_tmem_a(tmem + C::kTmemO + st * D, tmem + st * 128 + ks * 8,
-                                        umma_desc_mn_sw128(vb + ks * 2048, Tile::kBoxBytes, 1024),
-                                        kIdescO, !(first && ks == 0));
-                    umma_commit(&pv_done[st]);
-                    if (last) umma_commit(&empty[buf]);
-                    if (end) umma_commit(&o_done[st]);
-                    return true;
-                };
-                auto read_p = [&](int st) {              // P V has read P: S may overwrite it
-                    const bool done = wait(&pv_done[st], (pv_parity >> st) & 1u);
-                    pv_parity ^= 1u << st;
-                    return done;
-                };
-                if (pair) {
-                    ok = scores(0, 0, false) && scores(1, 0, true);
-                    for (int i = 0; ok && i < n; ++i)
-                        for (int st = 0; ok && st < 2; ++st) {
-                            ok = outputs(st, i, i == 0, st == 1, i == n - 1) && read_p(st);
-                            if (ok && i + 1 < n) ok = scores(st, i + 1, st == 1);
-                        }
-                } else {
-                    ok = scores(0, 0, true);
-                    if (ok && n > 1) ok = scores(1, 1, true);
-                    for (int i = 0; ok && i < n; ++i) {
-                        const int st = i & 1;
-                        ok = outputs(st, i, i < 2, true, i + 2 >= n) && read_p(st);
-                        if (ok && i + 2 < n) ok = scores(st, i + 2, true);
-                    }
-                }
-                base += 2 * n;
+                for (int ks = 0; ks < C::kStep / 16; ++ks)
+                    umma_f16_tmem_a_elected(leader, o_at, p_at + ks * 8, vd + ks * (2048 >> 4),
+                                            kIdescO, ks > 0 ? 1u : step > 0);
+                umma_commit_elected(leader, &pv_done[st]);
+                if (steps.last_of_tile(st, step)) umma_commit_elected(leader, &empty[buf]);
             }
-            umma_commit(drain);                          // before tensor memory is freed
-            mbar_wait_drain(drain, 0);
+            if (ok && !steps.takes_last(st) && lane == 0) {       // a tile without this stream
+                mbar_arrive(&empty[(base + prefix_k_pos(n - 1)) % C::kBufs]);
+                mbar_arrive(&empty[(base + prefix_v_pos(n - 1, n)) % C::kBufs]);
+            }
+            base += 2 * n;
         }
+        umma_commit_elected(leader, &drain[st]);           // before tensor memory is freed
+        __syncwarp();
+        mbar_wait_drain(&drain[st], 0);
         __syncwarp();
     } else if (warp >= C::kSoftmaxWarp) {
         // -------------------------------------------------------- softmax
@@ -469,12 +513,14 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
         const int st = swarp >> 2;
         const int row = (swarp & 3) * 32 + lane;         // of the stream: this thread's TMEM lane
         const uint32_t lanes = (uint32_t)((swarp & 3) * 32) << 16;
-        const uint32_t s_at = tmem + lanes + st * 128;
+        const uint32_t s_at = tmem + lanes + st * C::kStep;
+        const uint32_t p_at = tmem + lanes + C::kTmemP + st * (C::kStep / 2);
         const uint32_t o_at = tmem + lanes + C::kTmemO + st * D;
         const float scale = fabsf(p.scale_log2);
         const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;   // -q instead of -scale
-        uint32_t s_parity = 0, o_parity = 0;
-        long long base = 0;
+        uint32_t s_parity = 0, pv_parity = 0;
+        int runs = 0;
+        uint32_t base = 0;
         bool ok = true;
         while (wk.next(run)) {
             const int rt = run.row_tile;
@@ -523,18 +569,24 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
                         make_int4(slot_id, sharers, i * G, pair ? 0 : 1);
             }
 
+            // (a stream without a step in the last run may only now begin it)
+            if (runs > 0 && ok) ok = __all_sync(FULL, wait(q_seen, (uint32_t)(runs - 1) & 1u));
+            ++runs;
             // the queries, swizzled like a key tile; the last 32 rows are filled up
             // with zeros, and what lies behind them is nobody's
+            if (stid < n_rows) {
+                const int e = stid / G, u = unit_list[e];
+                q_rows[stid] = (u / p.top_k) * p.H_q + h * G + (stid - e * G);
+            }
+            named_barrier(1, C::kSoftmax);
             constexpr int kChunks = D / 8, kPass = C::kSoftmax / kChunks;
             const int c = stid % kChunks;
-#pragma unroll 4
+#pragma unroll 8
             for (int r = stid / kChunks; r < ((n_rows + 31) & ~31); r += kPass) {
                 uint4 x = make_uint4(0, 0, 0, 0);
                 if (r < n_rows) {
-                    const int e = r / G, u = unit_list[e];
-                    x = *reinterpret_cast<const uint4 *>(
-                        static_cast<const T *>(p.q) +
-                        ((size_t)(u / p.top_k) * p.H_q + (size_t)h * G + (r - e * G)) * D + c * 8);
+                    x = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) +
+                                                         (size_t)q_rows[r] * D + c * 8);
                     x.x ^= flip;
                     x.y ^= flip;
                     x.z ^= flip;
@@ -555,21 +607,35 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
             const int tile_row = (pair ? st * C::kStreamRows : 0) + (swarp & 3) * 32;
             const bool busy = tile_row < n_rows;          // this warp has rows
             float m_ref = -INFINITY, l0 = 0.f, l1 = 0.f;
-            int done = 0;
-            for (int i = pair ? 0 : st; i < n; i += pair ? 1 : 2) {
+            const PrefixSteps steps(pair, n, p.keys - (run.first + n - 1) * C::kTile);
+            const int count = steps.count(st);
+            for (int step = 0; step < count; ++step) {
                 if (ok) ok = __all_sync(FULL, wait(&s_full[st], s_parity));
                 s_parity ^= 1;
-                const int rows = min(C::kTile, p.keys - (run.first + i) * C::kTile);
-                if (rows < C::kTile) {
+                const int i = steps.tile(step);
+                const int rows = min(C::kStep, p.keys - (run.first + i) * C::kTile -
+                                                   steps.half(st, step) * C::kStep);
+                float s[C::kStep];
+                if (ok && busy) {
+                    tc_fence_after_sync();
+                    tmem_ld32(s_at, reinterpret_cast<float(&)[32]>(s[0]));
+                    tmem_ld32(s_at + 32, reinterpret_cast<float(&)[32]>(s[32]));
+                    tmem_ld_wait();
+                    tc_fence_before_sync();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_free[st]);
+                if (rows < C::kStep) {
                     // rows past the prefix hold other keys or nothing: zero V there
-                    // (0 * NaN) before any product with this tile's P.  Both streams
-                    // of a pair read the tile: they zero half each, and meet.
-                    const long long pos = base + prefix_v_pos(i, n);
+                    // (0 * NaN) before any product with this step's P.  Both streams
+                    // of a pair take the step: they zero half each, and meet.
+                    const uint32_t pos = base + prefix_v_pos(i, n);
                     const int buf = (int)(pos % C::kBufs);
-                    if (ok) ok = __all_sync(FULL, wait(&full[buf], (uint32_t)(pos / C::kBufs) & 1u));
+                    if (ok) ok = __all_sync(FULL, wait(&full[buf], (pos / C::kBufs) & 1u));
                     if (ok) {
-                        unsigned char *vt = smem + buf * C::kTileBytes;
-                        const int left = (C::kTile - rows) * Tile::kBoxes * 8;
+                        unsigned char *vt = smem + buf * C::kTileBytes +
+                                            steps.half(st, step) * C::kStep * 128;
+                        const int left = (C::kStep - rows) * Tile::kBoxes * 8;
                         for (int e = pair ? stid : stid & 127; e < left; e += pair ? 256 : 128) {
                             const int chunk = e & 7, bx = (e >> 3) % Tile::kBoxes;
                             const int key = rows + (e >> 3) / Tile::kBoxes;
@@ -580,28 +646,31 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
                     }
                     if (pair) named_barrier(1, C::kSoftmax);
                 }
+                float top = 0.f;
                 if (ok && busy) {
-                    tc_fence_after_sync();
-                    float top = -INFINITY;
+                    if (rows < C::kStep) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float s[32];
-                        tmem_ld32(s_at + c * 32, s);
-                        tmem_ld_wait();
-                        if (rows < C::kTile) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (c * 32 + e >= rows) s[e] = -INFINITY;
-                        }
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) top = fmaxf(top, s[e]);
+                        for (int e = 0; e < C::kStep; ++e)
+                            if (e >= rows) s[e] = -INFINITY;
                     }
-                    top *= scale;
-                    // the first tile sets the reference, later ones move it rarely
-                    const bool move = done == 0 || top > m_ref + kPrefixSlack;
+                    float tops[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                    for (int e = 4; e < C::kStep; ++e) tops[e & 3] = fmaxf(tops[e & 3], s[e]);
+                    top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * scale;
+                }
+                // the last step's product has read P, and O is up to date (warps without
+                // rows wait, too: their arrival for this step must not count for the last)
+                if (step > 0) {
+                    if (ok) ok = __all_sync(FULL, wait(&pv_done[st], pv_parity));
+                    pv_parity ^= 1;
+                }
+                if (ok && busy) {
+                    // the first step sets the reference, later ones move it rarely
+                    const bool move = step == 0 || top > m_ref + kPrefixSlack;
                     if (__any_sync(FULL, move)) {
                         const float m_new = move ? top : m_ref;
-                        if (done > 0) {
+                        if (step > 0) {
+                            tc_fence_after_sync();
                             const float a = move ? exp2_approx(m_ref - m_new) : 1.f;
                             l0 *= a;
                             l1 *= a;
@@ -619,27 +688,25 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
                     }
                     const float m0 = m_ref == -INFINITY ? 0.f : m_ref;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float s[32];
-                        tmem_ld32(s_at + c * 32, s);
-                        tmem_ld_wait();
+                    for (int c = 0; c < C::kStep / 32; ++c) {
                         uint32_t w[16];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            s[e] = exp2_approx(fmaf(s[e], scale, -m0));
-                            if (rows < C::kTile && c * 32 + e >= rows) s[e] = 0.f;
-                        }
-#pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            l0 += s[2 * e];
-                            l1 += s[2 * e + 1];
-                            w[e] = pack2<T>(s[2 * e], s[2 * e + 1]);
+                            float *x = s + c * 32 + 2 * e;
+                            x[0] = exp2_approx(fmaf(x[0], scale, -m0));
+                            x[1] = exp2_approx(fmaf(x[1], scale, -m0));
+                            if (rows < C::kStep) {       // (scale 0 makes NaN of -inf)
+                                if (c * 32 + 2 * e >= rows) x[0] = 0.f;
+                                if (c * 32 + 2 * e + 1 >= rows) x[1] = 0.f;
+                            }
+                            l0 += x[0];
+                            l1 += x[1];
+                            w[e] = pack2<T>(x[0], x[1]);
                         }
-                        tmem_st16(s_at + c * 16, w);
+                        tmem_st16(p_at + c * 16, w);
                     }
                     tmem_st_wait();
                 }
-                ++done;
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[st]);
@@ -647,17 +714,17 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
 
             // this run's partial state: rows of slot rt + block, the second stream's
             // behind the first's (its own rows, or the other half of the keys)
-            if (done > 0) {
-                if (ok) ok = __all_sync(FULL, wait(&o_done[st], o_parity));
-                o_parity ^= 1;
+            if (count > 0) {
+                if (ok) ok = __all_sync(FULL, wait(&pv_done[st], pv_parity));
+                pv_parity ^= 1;
             }
             if (tile_row + lane < n_rows) {
                 float *slot = p.parts.slots + (size_t)slot_id * p.parts.slot_floats;
                 const int r = st * C::kStreamRows + row;
                 *reinterpret_cast<float2 *>(slot + (size_t)C::kRows * D + 2 * r) =
-                    make_float2(ok && done > 0 ? m_ref : -INFINITY, l0 + l1);
+                    make_float2(ok && count > 0 ? m_ref : -INFINITY, l0 + l1);
             }
-            if (ok && done > 0 && busy) {
+            if (ok && count > 0 && busy) {
                 tc_fence_after_sync();
                 float *out = p.parts.slots + (size_t)slot_id * p.parts.slot_floats +
                              (size_t)(st * C::kStreamRows + row) * D;
@@ -685,20 +752,30 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
     }
 }
 
-// One output row per D/4 lanes, four elements a lane.  The parts' (m, l) are read
-// one per lane, so that all of them, their weights 2^(m - M) and the sum L cost one
-// trip to memory; then the lanes add up the weighted O rows, eight loads in flight.
-// More parts than lanes go in rounds, the sums rescaled in between.  The order is
-// fixed: suffix runs, then prefix runs.
-template <typename T, int D>
-__global__ void __launch_bounds__(256) sha_prefix_merge_kernel(const PrefixMergeParams p)
+// One output row per D/4 lanes and kWays warps, four elements a lane.  The parts of
+// a row go round its warps; each reads its parts' (m, l) one per lane, so that all
+// of them, their weights 2^(m - M) and the sum L cost one trip to memory, then the
+// lanes add up the weighted O rows, eight loads in flight.  More parts than lanes go
+// in rounds, the sums rescaled in between; the warps meet in shared memory.  The
+// order is fixed: suffix runs, then prefix runs.  A call of few rows takes kWays =
+// 4, for the loads in flight: four of a row's trips to memory become one.
+constexpr int kMergeThreads = 256;
+
+template <typename T, int D, int kWays>
+__global__ void __launch_bounds__(kMergeThreads) sha_prefix_merge_kernel(const PrefixMergeParams p)
 {
     constexpr int kLanes = D / 4;
+    constexpr int kRowsPerWarp = 32 / kLanes;
+    constexpr int kRowsPerBlock = kMergeThreads / 32 / kWays * kRowsPerWarp;
+    __shared__ float4 s_o[kWays > 1 ? kMergeThreads : 1];
+    __shared__ float2 s_ml[kWays > 1 ? kMergeThreads / kLanes : 1];
     const unsigned FULL = 0xffffffffu;
     const int G = p.H_q / p.H_kv;
-    const int sub = threadIdx.x % kLanes;
+    const int sub = threadIdx.x % kLanes, warp = threadIdx.x >> 5;
+    const int way = warp % kWays;
+    const int local = warp / kWays * kRowsPerWarp + (threadIdx.x & 31) / kLanes;
     const long long rows = (long long)p.B * p.top_k * G;
-    const long long at = ((long long)blockIdx.x * 256 + threadIdx.x) / kLanes;
+    const long long at = (long long)blockIdx.x * kRowsPerBlock + local;
     // (the call's inputs were complete before the passes began)
     const bool inside = at < rows;
     const int u = inside ? (int)(at / G) : 0, j = inside ? (int)(at - (long long)u * G) : 0;
@@ -715,14 +792,15 @@ __global__ void __launch_bounds__(256) sha_prefix_merge_kernel(const PrefixMerge
     }
     const int halves = 1 + ref.w;
     const int n = run.y + ref.y * halves;
-    int rounds = (n + kLanes - 1) / kLanes;
+    const int mine = (n - way + kWays - 1) / kWays;      // parts way, way + kWays, ...
+    int rounds = (mine + kLanes - 1) / kLanes;
     if (kLanes < 32) rounds = max(rounds, __shfl_xor_sync(FULL, rounds, 16));
 
     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
     float M = -INFINITY, L = 0.f;
     for (int r = 0; r < rounds; ++r) {
         // this lane's part: where its row of O is, its (m, l)
-        const int i = r * kLanes + sub;
+        const int i = (r * kLanes + sub) * kWays + way;
         const float *o = nullptr;
         float m = -INFINITY, l = 0.f;
         if (i < run.y) {
@@ -732,7 +810,8 @@ __global__ void __launch_bounds__(256) sha_prefix_merge_kernel(const PrefixMerge
             l = __ldcg(slot + G * D + G + j);
         } else if (i < n) {
             const int k = i - run.y;
-            const float *slot = p.parts.slots + (size_t)(ref.x + k / halves) * p.parts.slot_floats;
+            const float *slot =
+                p.parts.slots + (size_t)(ref.x + (k >> ref.w)) * p.parts.slot_floats;
             const int row = ref.z + j + (k & ref.w) * (p.parts.slot_rows / 2);
             o = slot + (size_t)row * D;
             const float2 ml = __ldcg(reinterpret_cast<const float2 *>(
@@ -757,7 +836,7 @@ __global__ void __launch_bounds__(256) sha_prefix_merge_kernel(const PrefixMerge
         O.y *= a;
         O.z *= a;
         O.w *= a;
-        int parts = min(n - r * kLanes, kLanes);
+        int parts = min(mine - r * kLanes, kLanes);
         if (kLanes < 32) parts = max(parts, __shfl_xor_sync(FULL, parts, 16));
 #pragma unroll 8
         for (int k = 0; k < parts; ++k) {
@@ -771,6 +850,30 @@ __global__ void __launch_bounds__(256) sha_prefix_merge_kernel(const PrefixMerge
                 O.z = fmaf(wk, x.z, O.z);
                 O.w = fmaf(wk, x.w, O.w);
             }
+        }
+    }
+    if constexpr (kWays > 1) {
+        s_o[threadIdx.x] = O;
+        if (sub == 0) s_ml[threadIdx.x / kLanes] = make_float2(M, L);
+        __syncthreads();
+        if (way > 0) return;
+        float top = M;
+#pragma unroll
+        for (int v = 1; v < kWays; ++v) top = fmaxf(top, s_ml[threadIdx.x / kLanes + v * kRowsPerWarp].x);
+        const float base = top == -INFINITY ? 0.f : top;
+        float a = exp2f(M - base);
+        O = make_float4(a * O.x, a * O.y, a * O.z, a * O.w);
+        L *= a;
+#pragma unroll
+        for (int v = 1; v < kWays; ++v) {
+            const float2 ml = s_ml[threadIdx.x / kLanes + v * kRowsPerWarp];
+            const float4 x = s_o[threadIdx.x + 32 * v];
+            a = exp2f(ml.x - base);
+            O.x = fmaf(a, x.x, O.x);
+            O.y = fmaf(a, x.y, O.y);
+            O.z = fmaf(a, x.z, O.z);
+            O.w = fmaf(a, x.w, O.w);
+            L = fmaf(a, ml.y, L);
         }
     }
     if (!live) return;

@@ -131,16 +131,56 @@ __device__ __forceinline__ void umma_f16(uint32_t tmem_d, uint64_t adesc, uint64
         : "memory");
 }
 
-// The same with A in tensor memory: 16-bit elements, row i in lane i, two
-// consecutive K elements per 32-bit column from tmem_a on (K = 16: 8 columns).
-__device__ __forceinline__ void umma_f16_tmem_a(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
-                                                uint32_t idesc, uint32_t accumulate)
+// One lane of a converged warp, for the forms below: the whole warp runs them and
+// only the elected lane issues.  The operands then stay in uniform registers; under
+// a branch of one lane each MMA first moves its descriptors there, 100 clocks each.
+__device__ __forceinline__ uint32_t elect_one()
 {
+    uint32_t pred;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(pred));
+    return pred;
+}
+
+__device__ __forceinline__ void umma_f16_elected(uint32_t leader, uint32_t tmem_d, uint64_t adesc,
+                                                 uint64_t bdesc, uint32_t idesc,
+                                                 uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
-        "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+
+// The same with A in tensor memory: 16-bit elements, row i in lane i, two
+// consecutive K elements per 32-bit column from tmem_a on (K = 16: 8 columns).
+__device__ __forceinline__ void umma_f16_tmem_a_elected(uint32_t leader, uint32_t tmem_d,
+                                                        uint32_t tmem_a, uint64_t bdesc,
+                                                        uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+
+__device__ __forceinline__ void umma_commit_elected(uint32_t leader, uint64_t *bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            smem_addr(bar)),
+        "r"(leader)
         : "memory");
 }
 
