@@ -959,9 +959,9 @@ sha_status_t launch_prefix(const sha::PrefixParams &prm, const void *k, const vo
                       tm_k, tm_v);
     if (e != cudaSuccess) return launch_error(e);
     const long long rows = (long long)prm.B * prm.top_k * (prm.H_q / prm.H_kv);
-    // four warps a row while that leaves all rows resident at once
+    // four warps a row while rows are few (up to four waves of resident blocks)
     const int per_warp = 32 / (D / 4), warps = sha::kMergeThreads / 32;
-    const bool four = rows <= (long long)num_sms * 16 * per_warp;
+    const bool four = rows <= (long long)num_sms * 64 * per_warp;
     const int per_block = four ? warps / 4 * per_warp : warps * per_warp;
     e = launch_kernel(four ? sha::sha_prefix_merge_kernel<T, D, 4> : sha::sha_prefix_merge_kernel<T, D, 1>,
                       (int)((rows + per_block - 1) / per_block), sha::kMergeThreads, 0, stream, merge);

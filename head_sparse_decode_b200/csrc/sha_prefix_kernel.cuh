@@ -114,7 +114,8 @@ struct PrefixConfig {
     static constexpr int kUnitOffset = kWarpOffset + 4 * 8;         // a row tile's units
     static constexpr int kQRowOffset = kUnitOffset + 4 * kRows;     // and the rows of q they are
     static constexpr int kStartOffset = kQRowOffset + 4 * kRows;    // first row tile of each head
-    static constexpr int kSmemBytes = 1024 + kStartOffset + 4 * (kPrefixMaxHeads + 1);
+    static constexpr int kPairOffset = kStartOffset + 4 * (kPrefixMaxHeads + 1);
+    static constexpr int kSmemBytes = 1024 + kPairOffset + 4 * (kPrefixMaxHeads + 1);
     // tensor memory: S of the two streams, P, then O
     static constexpr int kTmemCols = 512;
     static constexpr int kTmemP = 2 * kStep;
@@ -128,11 +129,12 @@ struct PrefixConfig {
 // (log2 units): P stays below 2^8, far inside fp16.
 constexpr float kPrefixSlack = 8.f;
 
-// First row tile of every head (start[H_kv] = all of them), from the histogram
-// of the selection.  All threads of the block; ends with a barrier.
+// First row tile of every head (start[H_kv] = all of them), and how many row tiles
+// of more than 128 rows come before it (pairs[H_kv] = all of those), from the
+// histogram of the selection.  All threads of the block; ends with a barrier.
 template <int NT>
-__device__ __forceinline__ void prefix_row_tiles(const PrefixParams &p, int units_per_tile,
-                                                 int *start)
+__device__ __forceinline__ void prefix_row_tiles(const PrefixParams &p, int G, int units_per_tile,
+                                                 int *start, int *pairs)
 {
     const int tid = threadIdx.x;
     for (int h = tid; h <= p.H_kv; h += NT) start[h] = 0;
@@ -147,19 +149,30 @@ __device__ __forceinline__ void prefix_row_tiles(const PrefixParams &p, int unit
             if ((unsigned)h[i] < (unsigned)p.H_kv) atomicAdd(&start[h[i]], 1);
     }
     __syncthreads();
-    if (tid < 32) {                                  // counts -> exclusive sums of row tiles
-        int base = 0;
+    if (tid < 32) {                                  // counts -> exclusive sums
+        int base = 0, pair_base = 0;
         for (int h0 = 0; h0 <= p.H_kv; h0 += 32) {
             const int h = h0 + tid;
-            const int n = h < p.H_kv ? (start[h] + units_per_tile - 1) / units_per_tile : 0;
-            int incl = n;
+            const int count = h < p.H_kv ? start[h] : 0;
+            const int n = (count + units_per_tile - 1) / units_per_tile;
+            // all but a head's last row tile are full
+            const int m = n > 0 ? n - 1 + ((count - (n - 1) * units_per_tile) * G > 128) : 0;
+            int incl = n, pair_incl = m;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const int x = __shfl_up_sync(0xffffffffu, incl, off);
-                if (tid >= off) incl += x;
+                const int y = __shfl_up_sync(0xffffffffu, pair_incl, off);
+                if (tid >= off) {
+                    incl += x;
+                    pair_incl += y;
+                }
             }
-            if (h <= p.H_kv) start[h] = base + incl - n;
+            if (h <= p.H_kv) {
+                start[h] = base + incl - n;
+                pairs[h] = pair_base + pair_incl - m;
+            }
             base += __shfl_sync(0xffffffffu, incl, 31);
+            pair_base += __shfl_sync(0xffffffffu, pair_incl, 31);
         }
     }
     __syncthreads();
@@ -167,57 +180,92 @@ __device__ __forceinline__ void prefix_row_tiles(const PrefixParams &p, int unit
 
 // How the row tiles x key tiles are cut over the blocks: contiguous ranges of the
 // tiles, numbered row-tile-major.  Beginning a run (its list, its queries, its
-// state written out) takes a block about as long as kRunTiles key tiles, so whole
-// row tiles, or equal pieces of them, go to the blocks where the busiest then has
-// no more to do than under the even cut, which gives most blocks two runs.
-// (OPT-66B-shaped, 72 row tiles of 15 key tiles: 2 pieces of 7 or 8 each, 144
-// runs, against 219.)  All in 32 bits -- the host keeps the tiles of a call below
-// 2^31 -- since a 64-bit division costs a lone thread 0.4 us.
+// state written out) takes a block about as long as kRunTiles key tiles, so equal
+// pieces of row tiles go to the blocks, one each, where there are enough blocks:
+// twice as many pieces of a row tile of more than 128 rows, whose key tiles take
+// twice the products (16K document, heads with 256 + 64 rows: 26 us against 37 with
+// pieces alike), and no more pieces than the longest one needs, since each leaves a
+// state to be merged.  (OPT-66B-shaped, 72 row tiles of 15 key tiles: 2 pieces of 7
+// or 8 each, 144 runs, against 219 under the even cut.)  With more row tiles than
+// blocks, whole row tiles or an even cut of the tiles.  All in 32 bits -- the host
+// keeps the tiles of a call below 2^31 -- since a 64-bit division costs a lone
+// thread 0.4 us.
 constexpr unsigned kRunTiles = 3;
 
-// A run: tiles [first, first + n) of row tile `row_tile`.
+// A run: tiles [first, first + n) of row tile `row_tile`, of head `head`.
 struct PrefixRun {
-    int row_tile, first, n;
+    int row_tile, head, first, n;
 };
 
 struct PrefixCut {
-    unsigned key_tiles, blocks;
-    unsigned pieces;             // > 0: a row tile is cut into this many, one per block
+    const int *start, *pairs;    // of the heads (prefix_row_tiles)
+    int heads;
+    unsigned key_tiles;
+    unsigned pieces, pieces2;    // > 0: pieces of a row tile of up to, of more than 128 rows
     unsigned base, extra;        // else block c has base tiles, the first `extra` one more
     unsigned t, t_end;           // this block's range
+    int own_pieces;              // (pieces) those of this block's row tile
 
     __device__ __forceinline__ unsigned begin(unsigned c) const
     {
         return c * base + min(c, extra);
     }
-    __device__ __forceinline__ void plan(unsigned row_tiles, unsigned tiles, unsigned grid,
-                                         unsigned block)
+    // First block of head h, under pieces.
+    __device__ __forceinline__ unsigned block_of(int h) const
     {
-        key_tiles = tiles;
-        const unsigned total = row_tiles * tiles;
-        blocks = min(total, grid);
-        pieces = 0;
-        base = extra = t = t_end = 0;
-        if (total == 0) return;
-        const unsigned even = (total + blocks - 1) / blocks + 2 * kRunTiles;
-        if (row_tiles <= blocks) {
-            const unsigned p = min(blocks / row_tiles, tiles);
-            if ((tiles + p - 1) / p + kRunTiles <= even) {
-                pieces = p;
-                blocks = row_tiles * p;
-            }
+        return (unsigned)start[h] * pieces + (unsigned)pairs[h] * (pieces2 - pieces);
+    }
+    // The last head whose first f(head) is at most x: among equal ones the last is
+    // the one that has row tiles.
+    template <class F>
+    __device__ __forceinline__ int search(unsigned x, F f) const
+    {
+        int lo = 0, hi = heads;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (f(mid) <= x) lo = mid;
+            else hi = mid;
         }
-        if (pieces) {
-            if (block < blocks) {
-                const unsigned r = block / pieces, k = block - r * pieces;
-                const unsigned b = tiles / pieces, x = tiles - b * pieces;
-                t = r * tiles + k * b + min(k, x);
-                t_end = t + b + (k < x);
+        return lo;
+    }
+    __device__ __forceinline__ void plan(const int *start_, const int *pairs_, int heads_,
+                                         unsigned tiles, unsigned grid, unsigned block)
+    {
+        start = start_;
+        pairs = pairs_;
+        heads = heads_;
+        key_tiles = tiles;
+        pieces = pieces2 = base = extra = t = t_end = 0;
+        const unsigned row_tiles = (unsigned)start[heads], wide = (unsigned)pairs[heads];
+        const unsigned total = row_tiles * tiles;
+        if (total == 0) return;
+        const unsigned weight = row_tiles + wide;
+        if (weight <= grid) {
+            // the longest piece of each kind, then as few pieces as keep to it
+            const unsigned p1 = min(grid / weight, tiles), p2 = min(2 * grid / weight, tiles);
+            const unsigned q1 = (tiles + p1 - 1) / p1, q2 = (tiles + p2 - 1) / p2;
+            pieces = (tiles + q1 - 1) / q1;
+            pieces2 = (tiles + q2 - 1) / q2;
+            if (block >= block_of(heads)) return;
+            const int h = search(block, [&](int x) { return block_of(x); });
+            unsigned k = block - block_of(h);
+            const unsigned wide_tiles = (unsigned)(pairs[h + 1] - pairs[h]);
+            unsigned r = k / pieces2, own = pieces2;
+            if (r >= wide_tiles) {               // the last row tile, of up to 128 rows
+                r = wide_tiles;
+                own = pieces;
             }
+            k -= r * pieces2;
+            const unsigned b = tiles / own, x = tiles - b * own;
+            t = ((unsigned)start[h] + r) * tiles + k * b + min(k, x);
+            t_end = t + b + (k < x);
+            own_pieces = (int)own;
             return;
         }
+        const unsigned blocks = min(total, grid);
+        const unsigned even = (total + blocks - 1) / blocks + 2 * kRunTiles;
         const unsigned whole = (row_tiles + blocks - 1) / blocks;
-        if (row_tiles > blocks && whole * (tiles + kRunTiles) <= even) {
+        if (whole * (tiles + kRunTiles) <= even) {
             t = min(block * whole, row_tiles) * tiles;
             t_end = min((block + 1) * whole, row_tiles) * tiles;
             base = whole * tiles;                    // begin() of a block in use
@@ -234,6 +282,7 @@ struct PrefixCut {
     {
         if (t >= t_end) return false;
         r.row_tile = (int)(t / key_tiles);
+        r.head = search((unsigned)r.row_tile, [&](int x) { return (unsigned)start[x]; });
         const unsigned end = ((unsigned)r.row_tile + 1) * key_tiles;
         r.first = (int)(t - (unsigned)r.row_tile * key_tiles);
         r.n = (int)(min(end, t_end) - t);
@@ -244,25 +293,13 @@ struct PrefixCut {
     __device__ __forceinline__ int sharers(const PrefixRun &r, unsigned block) const
     {
         if (r.first + r.n == (int)key_tiles) return 1;
-        if (pieces) return (int)pieces;
+        if (pieces) return own_pieces;
         const unsigned last = ((unsigned)r.row_tile + 1) * key_tiles - 1;
         const unsigned split = extra * (base + 1);
         const unsigned c = last < split ? last / (base + 1) : extra + (last - split) / base;
         return (int)(c - block) + 1;
     }
 };
-
-// The head of row tile r: the last h with start[h] <= r among those that have tiles.
-__device__ __forceinline__ int prefix_head_of(const int *start, int H_kv, int r)
-{
-    int lo = 0, hi = H_kv;                           // start[lo] <= r < start[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (start[mid] <= r) lo = mid;
-        else hi = mid;
-    }
-    return lo;
-}
 
 // Ring position of a run's K and V tiles: K_0, then K_i, V_(i-1) for i = 1 .. n-1,
 // then V_(n-1) -- the order in which the products use them.
@@ -323,6 +360,7 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
     int *unit_list = reinterpret_cast<int *>(smem + C::kUnitOffset);
     int *q_rows = reinterpret_cast<int *>(smem + C::kQRowOffset);
     int *start = reinterpret_cast<int *>(smem + C::kStartOffset);
+    int *pairs = reinterpret_cast<int *>(smem + C::kPairOffset);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
     const int G = p.H_q / p.H_kv;
@@ -357,9 +395,9 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
     pdl_wait();
     pdl_launch_dependents();
 
-    prefix_row_tiles<C::kThreads>(p, units_per_tile, start);
+    prefix_row_tiles<C::kThreads>(p, G, units_per_tile, start, pairs);
     PrefixCut wk;
-    wk.plan((unsigned)start[p.H_kv], (unsigned)((p.keys + C::kTile - 1) / C::kTile), gridDim.x,
+    wk.plan(start, pairs, p.H_kv, (unsigned)((p.keys + C::kTile - 1) / C::kTile), gridDim.x,
             blockIdx.x);
     PrefixRun run;
 
@@ -385,7 +423,7 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
         bool ok = true;
         const int box_rows = min(p.page_size, C::kTile);
         while (ok && wk.next(run)) {
-            const int h = prefix_head_of(start, p.H_kv, run.row_tile);
+            const int h = run.head;
             const int n = run.n;
             for (int i = 0; ok && i < 2 * n; ++i) {
                 // position i is K_0, K_((i+1)/2) (odd i < 2n-1) or V
@@ -524,7 +562,7 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
         bool ok = true;
         while (wk.next(run)) {
             const int rt = run.row_tile;
-            const int h = prefix_head_of(start, p.H_kv, rt);
+            const int h = run.head;
             // this row tile's units: those of the head's units, in order, that the
             // tiles before it have not taken
             const int rank0 = (rt - start[h]) * units_per_tile;
