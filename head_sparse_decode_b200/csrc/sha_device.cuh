@@ -278,6 +278,20 @@ __device__ __forceinline__ void named_barrier(int id, int threads)
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// Arrive on it without waiting; `threads` counts those that wait, too.
+__device__ __forceinline__ void named_barrier_arrive(int id, int threads)
+{
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Eight floats in one 32-byte store, a whole sector of one row; dst 32-byte aligned.
+__device__ __forceinline__ void store8(float *dst, const float *v)
+{
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(v[0]),
+                 "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
+
 // ---- programmatic dependent launch ------------------------------------------
 // A kernel launched with programmatic stream serialization may start while the
 // previous kernel in the stream is still running.  pdl_wait() blocks until that

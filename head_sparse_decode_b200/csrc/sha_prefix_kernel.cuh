@@ -558,6 +558,7 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
         const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;   // -q instead of -scale
         uint32_t s_parity = 0, pv_parity = 0;
         int runs = 0;
+        if (st == 1) named_barrier_arrive(2, C::kSoftmax);      // stream 0 has the first turn
         uint32_t base = 0;
         bool ok = true;
         while (wk.next(run)) {
@@ -617,23 +618,31 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
                 q_rows[stid] = (u / p.top_k) * p.H_q + h * G + (stid - e * G);
             }
             named_barrier(1, C::kSoftmax);
-            constexpr int kChunks = D / 8, kPass = C::kSoftmax / kChunks;
+            constexpr int kChunks = D / 8, kPass = C::kSoftmax / kChunks, kBatch = 8;
             const int c = stid % kChunks;
-#pragma unroll 8
-            for (int r = stid / kChunks; r < ((n_rows + 31) & ~31); r += kPass) {
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (r < n_rows) {
-                    x = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) +
-                                                         (size_t)q_rows[r] * D + c * 8);
-                    x.x ^= flip;
-                    x.y ^= flip;
-                    x.z ^= flip;
-                    x.w ^= flip;
+            for (int r0 = stid / kChunks; r0 < ((n_rows + 31) & ~31); r0 += kBatch * kPass) {
+                uint4 x[kBatch];                          // all on the way before the first is stored
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int r = r0 + i * kPass;
+                    x[i] = make_uint4(0, 0, 0, 0);
+                    if (r < n_rows)
+                        x[i] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) +
+                                                                (size_t)q_rows[r] * D + c * 8);
                 }
-                const int rr = r & (C::kStreamRows - 1);
-                *reinterpret_cast<uint4 *>(smem + C::kQOffset + (r >> 7) * C::kQBytes +
-                                           (c >> 3) * Tile::kBoxBytes + rr * 128 +
-                                           (((c & 7) ^ (rr & 7)) << 4)) = x;
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int r = r0 + i * kPass, rr = r & (C::kStreamRows - 1);
+                    if (r < ((n_rows + 31) & ~31)) {
+                        x[i].x ^= flip;
+                        x[i].y ^= flip;
+                        x[i].z ^= flip;
+                        x[i].w ^= flip;
+                        *reinterpret_cast<uint4 *>(smem + C::kQOffset + (r >> 7) * C::kQBytes +
+                                                   (c >> 3) * Tile::kBoxBytes + rr * 128 +
+                                                   (((c & 7) ^ (rr & 7)) << 4)) = x[i];
+                    }
+                }
             }
             if (stid == 0) *paired = pair;
             fence_proxy_async_shared();
@@ -693,7 +702,12 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
                     }
                     float tops[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                    for (int e = 4; e < C::kStep; ++e) tops[e & 3] = fmaxf(tops[e & 3], s[e]);
+                    for (int e = 4; e + 4 < C::kStep; e += 8)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)      // (three-operand maxima)
+                            tops[i] = fmaxf(fmaxf(tops[i], s[e + i]), s[e + 4 + i]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tops[i] = fmaxf(tops[i], s[C::kStep - 4 + i]);
                     top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * scale;
                 }
                 // the last step's product has read P, and O is up to date (warps without
@@ -724,6 +738,12 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
                         }
                         m_ref = m_new;
                     }
+                }
+                // the streams of a pair take turns at the exponentials: each then has the
+                // unit, which they saturate, to itself while the other one reads its next
+                // scores (1500 clocks a step against 2360 in step with each other)
+                if (pair) named_barrier(2 + st, C::kSoftmax);
+                if (ok && busy) {
                     const float m0 = m_ref == -INFINITY ? 0.f : m_ref;
 #pragma unroll
                     for (int c = 0; c < C::kStep / 32; ++c) {
@@ -743,8 +763,9 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
                         }
                         tmem_st16(p_at + c * 16, w);
                     }
-                    tmem_st_wait();
                 }
+                if (pair) named_barrier_arrive(3 - st, C::kSoftmax);
+                if (ok && busy) tmem_st_wait();
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[st]);
@@ -773,9 +794,7 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
                     tmem_ld_wait();
                     if (tile_row + lane < n_rows) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4 *>(out + c * 32 + e) =
-                                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        for (int e = 0; e < 32; e += 8) store8(out + c * 32 + e, o + e);
                     }
                 }
             }
