@@ -287,24 +287,73 @@ def sha_decode_prefix(q, k_pages, v_pages, batch_head_index, seqlens, block_tabl
     rows cover the whole sequences, their entries for the prefix unread.  workspace
     (default: a new tensor) is uint8, at least sha_decode_prefix_workspace_size bytes;
     calls that share it must not overlap."""
+    pool, q_shape, dtype, index = k_pages.shape, q.shape, k_pages.dtype, k_pages.get_device()
+    code, i32 = _DTYPE_CODES.get(dtype), torch.int32
+    idx_shape, table_shape = batch_head_index.shape, block_table.shape
+    B = q_shape[0]
+    # one pass over what has to hold; a call that fails it is explained step by step
+    if not (index >= 0 and code is not None and len(pool) == 4 and v_pages.shape == pool
+            and (len(q_shape) == 3 or (len(q_shape) == 4 and q_shape[2] == 1))
+            and q_shape[-1] == pool[3] and out.numel() == B * q_shape[1] * pool[3]
+            and len(idx_shape) == 2 and idx_shape[0] == B and len(table_shape) == 2
+            and table_shape[0] == B and seqlens.shape == (B,) and prefix_table.dim() == 1
+            and 1 <= prefix_len <= prefix_table.shape[0] * pool[2]
+            and q.dtype is dtype and v_pages.dtype is dtype and out.dtype is dtype
+            and batch_head_index.dtype is i32 and seqlens.dtype is i32
+            and block_table.dtype is i32 and prefix_table.dtype is i32
+            and q.get_device() == index and v_pages.get_device() == index
+            and out.get_device() == index and batch_head_index.get_device() == index
+            and seqlens.get_device() == index and block_table.get_device() == index
+            and prefix_table.get_device() == index
+            and q.is_contiguous() and k_pages.is_contiguous() and v_pages.is_contiguous()
+            and out.is_contiguous() and batch_head_index.is_contiguous()
+            and seqlens.is_contiguous() and block_table.is_contiguous()
+            and prefix_table.is_contiguous()):
+        _explain_prefix(q, k_pages, v_pages, batch_head_index, seqlens, block_table, prefix_len,
+                        prefix_table, out)
+        code = _dtype_code(dtype)
+    num_pages, H_kv, page_size, d = pool
+    H_q, top_k = q_shape[1], idx_shape[1]
+    dev = k_pages.device
+    handle = _raw_stream(stream, dev)
+    if workspace is None:
+        nbytes = _prefix_workspace_size(B, H_q, H_kv, d, top_k, index)
+        workspace = seqlens.new_empty((nbytes + 3) // 4)
+        if stream is not None and handle != torch._C._cuda_getCurrentRawStream(index):
+            workspace.record_stream(torch.cuda.ExternalStream(handle, device=dev))
+    else:
+        if workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+        nbytes = workspace.numel() * workspace.element_size()
+    _on_device(dev, _lib.sha_decode_prefix,
+               (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), batch_head_index.data_ptr(),
+                seqlens.data_ptr(), block_table.data_ptr(), prefix_table.data_ptr(), prefix_len, B,
+                H_q, H_kv, num_pages, page_size, table_shape[1], d, top_k,
+                _default_scale(scale, d), out.data_ptr(), code, workspace.data_ptr(), nbytes,
+                handle))
+    return out
+
+
+def _explain_prefix(q, k_pages, v_pages, batch_head_index, seqlens, block_table, prefix_len,
+                    prefix_table, out):
+    index, dtype = k_pages.get_device(), k_pages.dtype
     if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
         raise ValueError("k_pages and v_pages must both be [num_pages, H_kv, page_size, d]")
-    num_pages, H_kv, page_size, d = k_pages.shape
-    dev, dtype, index = k_pages.device, k_pages.dtype, k_pages.get_device()
     if index < 0:
         raise ValueError("k_pages must be a CUDA tensor")
+    _dtype_code(dtype)
+    page_size, d = k_pages.shape[2], k_pages.shape[3]
     if q.dim() == 4 and q.shape[2] != 1:
         raise ValueError("decode takes one query token: q must be [B, H_q, 1, d]")
     if q.dim() not in (3, 4) or q.shape[-1] != d:
         raise ValueError("q must be [B, H_q, d] or [B, H_q, 1, d]")
-    B, H_q = q.shape[0], q.shape[1]
-    if out.numel() != B * H_q * d:
+    B = q.shape[0]
+    if out.numel() != B * q.shape[1] * d:
         raise ValueError("out must hold [B, H_q, d] elements")
     if batch_head_index.dim() != 2 or batch_head_index.shape[0] != B:
         raise ValueError("batch_head_index must be [B, top_k]")
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [B, max_pages]")
-    prefix_len = int(prefix_len)
     if prefix_len < 1:
         raise ValueError("prefix_len must be at least 1 (without a prefix: sha_decode_paged)")
     if prefix_table.dim() != 1 or prefix_table.shape[0] * page_size < prefix_len:
@@ -319,23 +368,6 @@ def sha_decode_prefix(q, k_pages, v_pages, batch_head_index, seqlens, block_tabl
     _check_contiguous("seqlens", seqlens, 1, torch.int32, index)
     _check_contiguous("block_table", block_table, 2, torch.int32, index)
     _check_contiguous("prefix_table", prefix_table, 1, torch.int32, index)
-    top_k = batch_head_index.shape[1]
-    code = _dtype_code(dtype)
-    handle = _raw_stream(stream, dev)
-    if workspace is None:
-        nbytes = _prefix_workspace_size(B, H_q, H_kv, d, top_k, index)
-        workspace = seqlens.new_empty((nbytes + 3) // 4)
-        if stream is not None and handle != torch._C._cuda_getCurrentRawStream(index):
-            workspace.record_stream(torch.cuda.ExternalStream(handle, device=dev))
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    _on_device(dev, _lib.sha_decode_prefix,
-               (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), batch_head_index.data_ptr(),
-                seqlens.data_ptr(), block_table.data_ptr(), prefix_table.data_ptr(), prefix_len, B,
-                H_q, H_kv, num_pages, page_size, block_table.shape[1], d, top_k,
-                _default_scale(scale, d), out.data_ptr(), code, workspace.data_ptr(),
-                workspace.numel() * workspace.element_size(), handle))
-    return out
 
 
 _lib.sha_decode_tokens.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i,
@@ -365,6 +397,9 @@ def _dtype_code(dtype):
     if dtype == torch.bfloat16:
         return SHA_BF16
     raise TypeError(f"unsupported dtype {dtype}")
+
+
+_DTYPE_CODES = {torch.float16: SHA_FP16, torch.bfloat16: SHA_BF16}
 
 
 def sha_decode_workspace_size(B, H_q, H_kv, N_kv, d, top_k, num_splits=0, device=None):
@@ -722,21 +757,41 @@ def sha_rope(x, positions, inv_freq, out=None, interleaved=False, mscale=1.0, st
     positions int32 [T], inv_freq float64 [rotary/2] (rope_frequencies), all on one
     device.  out (default: a new contiguous tensor) may be x itself.  Rotating by
     -positions is the inverse up to mscale^2, and the gradient."""
-    index, dtype = x.get_device(), x.dtype
-    xs = _check_heads_view("x", x, dtype, index)
-    T, H, d = x.shape
-    _check_vector("positions", positions, T, index)
-    _check_contiguous("inv_freq", inv_freq, 1, torch.float64, index)
+    shape, index, dtype = x.shape, x.get_device(), x.dtype
+    xs = x.stride()
+    code = _DTYPE_CODES.get(dtype)
+    # one pass over what has to hold; a call that fails it is explained step by step
+    if not (index >= 0 and code is not None and len(shape) == 3 and xs[2] == 1
+            and positions.dtype is torch.int32 and positions.get_device() == index
+            and positions.shape == shape[:1] and positions.is_contiguous()
+            and inv_freq.dtype is torch.float64 and inv_freq.get_device() == index
+            and inv_freq.dim() == 1 and inv_freq.is_contiguous()
+            and (out is None or (out.shape == shape and out.dtype is dtype
+                                 and out.get_device() == index and out.stride(2) == 1))):
+        _explain_rope(x, positions, inv_freq, out)
+        code = _dtype_code(dtype)
+    T, H, d = shape
     if out is None:
-        out = x.new_empty((T, H, d))
-    elif out.shape != x.shape:
-        raise ValueError("out must have x's shape")
-    os_ = _check_heads_view("out", out, dtype, index)
-    _on_device(x.device, _lib.sha_rope,
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    os_ = out.stride()
+    device = x.device
+    _on_device(device, _lib.sha_rope,
                (x.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), T, H, d,
-                2 * inv_freq.shape[0], 1 if interleaved else 0, mscale, xs, out.data_ptr(), os_,
-                _dtype_code(dtype), _raw_stream(stream, x.device)))
+                2 * inv_freq.shape[0], 1 if interleaved else 0, mscale, _stride_pair(xs[0], xs[1]),
+                out.data_ptr(), _stride_pair(os_[0], os_[1]), code, _raw_stream(stream, device)))
     return out
+
+
+def _explain_rope(x, positions, inv_freq, out):
+    index, dtype = x.get_device(), x.dtype
+    _check_heads_view("x", x, dtype, index)
+    _dtype_code(dtype)
+    _check_vector("positions", positions, x.shape[0], index)
+    _check_contiguous("inv_freq", inv_freq, 1, torch.float64, index)
+    if out is not None:
+        _check_heads_view("out", out, dtype, index)
+        if out.shape != x.shape:
+            raise ValueError("out must have x's shape")
 
 
 def sha_append_paged(k, v, k_pages, v_pages, block_table, positions, rows=None, inv_freq=None,
@@ -748,49 +803,79 @@ def sha_append_paged(k, v, k_pages, v_pages, block_table, positions, rows=None, 
     inv_freq (float64 [rotary/2]) keys turn by their position on the way, and q
     [T, H_q, d] turns into q_out (default: a new tensor; may be q itself).  Returns
     q_out (None without q)."""
+    shape, index, dtype = k.shape, k.get_device(), k.dtype
+    ks, vs, pool = k.stride(), v.stride(), k_pages.shape
+    code, i32 = _DTYPE_CODES.get(dtype), torch.int32
+    # one pass over what has to hold; a call that fails it is explained step by step
+    if not (index >= 0 and code is not None and len(shape) == 3 and v.shape == shape
+            and ks[2] == 1 and vs[2] == 1 and v.dtype is dtype and v.get_device() == index
+            and len(pool) == 4 and pool[1] == shape[1] and pool[3] == shape[2]
+            and v_pages.shape == pool and k_pages.dtype is dtype and v_pages.dtype is dtype
+            and k_pages.get_device() == index and v_pages.get_device() == index
+            and k_pages.is_contiguous() and v_pages.is_contiguous()
+            and block_table.dtype is i32 and block_table.get_device() == index
+            and block_table.dim() == 2 and block_table.is_contiguous()
+            and positions.dtype is i32 and positions.get_device() == index
+            and positions.shape == shape[:1] and positions.is_contiguous()
+            and (rows is None or (rows.dtype is i32 and rows.get_device() == index
+                                  and rows.shape == shape[:1] and rows.is_contiguous()))
+            and (inv_freq is None or (inv_freq.dtype is torch.float64 and inv_freq.dim() == 1
+                                      and inv_freq.get_device() == index
+                                      and inv_freq.is_contiguous()))):
+        _explain_append(k, v, k_pages, v_pages, block_table, positions, rows, inv_freq)
+        code = _dtype_code(dtype)
+    T, H_kv, d = shape
+    rotary, freq = (0, None) if inv_freq is None else (2 * inv_freq.shape[0], inv_freq.data_ptr())
+    H_q, qp, qs, op, os_ = 0, None, None, None, None
+    if q is not None:
+        q_shape, qs = q.shape, q.stride()
+        if inv_freq is None:
+            raise ValueError("q needs inv_freq: without a rotation there is nothing to do to it")
+        if not (len(q_shape) == 3 and q_shape[0] == T and q_shape[2] == d and qs[2] == 1
+                and q.dtype is dtype and q.get_device() == index):
+            _check_heads_view("q", q, dtype, index)
+            if q_shape[0] != T or q_shape[2] != d:
+                raise ValueError("q must be [T, H_q, d]")
+        if q_out is None:
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        else:
+            _check_heads_view("q_out", q_out, dtype, index)
+            if q_out.shape != q_shape:
+                raise ValueError("q_out must have q's shape")
+        os_ = q_out.stride()
+        H_q, qp, op = q_shape[1], q.data_ptr(), q_out.data_ptr()
+        qs, os_ = _stride_pair(qs[0], qs[1]), _stride_pair(os_[0], os_[1])
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    B, max_pages = block_table.shape
+    device = k.device
+    _on_device(device, _lib.sha_append_paged,
+               (k.data_ptr(), v.data_ptr(), _stride_pair(ks[0], ks[1]), _stride_pair(vs[0], vs[1]),
+                T, H_kv, d, k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+                None if rows is None else rows.data_ptr(), positions.data_ptr(), B, pool[0], pool[2],
+                max_pages, freq, rotary, 1 if interleaved else 0, mscale, qp, qs, H_q, op, os_, code,
+                _raw_stream(stream, device)))
+    return q_out
+
+
+def _explain_append(k, v, k_pages, v_pages, block_table, positions, rows, inv_freq):
     index, dtype = k.get_device(), k.dtype
-    ks = _check_heads_view("k", k, dtype, index)
-    vs = _check_heads_view("v", v, dtype, index)
-    T, H_kv, d = k.shape
+    _check_heads_view("k", k, dtype, index)
+    _dtype_code(dtype)
+    _check_heads_view("v", v, dtype, index)
     if v.shape != k.shape:
         raise ValueError("v must have k's shape")
     _check_contiguous("k_pages", k_pages, 4, dtype, index)
     _check_contiguous("v_pages", v_pages, 4, dtype, index)
-    num_pages, page_heads, page_size, page_d = k_pages.shape
-    if page_heads != H_kv or page_d != d or v_pages.shape != k_pages.shape:
+    if k_pages.shape[1] != k.shape[1] or k_pages.shape[3] != k.shape[2] \
+            or v_pages.shape != k_pages.shape:
         raise ValueError("k_pages and v_pages must both be [num_pages, H_kv, page_size, d]")
     _check_contiguous("block_table", block_table, 2, torch.int32, index)
-    _check_vector("positions", positions, T, index)
-    rp, rotary, freq = None, 0, None
+    _check_vector("positions", positions, k.shape[0], index)
     if rows is not None:
-        _check_vector("rows", rows, T, index)
-        rp = rows.data_ptr()
+        _check_vector("rows", rows, k.shape[0], index)
     if inv_freq is not None:
         _check_contiguous("inv_freq", inv_freq, 1, torch.float64, index)
-        rotary, freq = 2 * inv_freq.shape[0], inv_freq.data_ptr()
-    H_q, qp, qs, op, os_ = 0, None, None, None, None
-    if q is not None:
-        if inv_freq is None:
-            raise ValueError("q needs inv_freq: without a rotation there is nothing to do to it")
-        qs = _check_heads_view("q", q, dtype, index)
-        shape = q.shape
-        if shape[0] != T or shape[2] != d:
-            raise ValueError("q must be [T, H_q, d]")
-        if q_out is None:
-            q_out = q.new_empty(shape)
-        elif q_out.shape != shape:
-            raise ValueError("q_out must have q's shape")
-        os_ = _check_heads_view("q_out", q_out, dtype, index)
-        H_q, qp, op = shape[1], q.data_ptr(), q_out.data_ptr()
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    B, max_pages = block_table.shape
-    _on_device(k.device, _lib.sha_append_paged,
-               (k.data_ptr(), v.data_ptr(), ks, vs, T, H_kv, d, k_pages.data_ptr(),
-                v_pages.data_ptr(), block_table.data_ptr(), rp, positions.data_ptr(), B, num_pages,
-                page_size, max_pages, freq, rotary, 1 if interleaved else 0, mscale, qp, qs, H_q, op,
-                os_, _dtype_code(dtype), _raw_stream(stream, k.device)))
-    return q_out
 
 
 def sha_get_device_status(stream=None, device=None):

@@ -20,12 +20,15 @@ int pairs_per_item(int rotary)
     return pairs % 8 == 0 ? 8 : pairs % 4 == 0 ? 4 : pairs % 2 == 0 ? 2 : 1;
 }
 
-// Tokens and heads of a block.  A block wants about four items a thread, so that
-// its angles are shared by many heads; but a call that then has fewer blocks
-// than the device has SMs takes smaller blocks (each repeating its tokens'
-// angles), since it is latency that bounds it.
+// Tokens and heads of a block.  A block of a rotation wants about four items a
+// thread, so that its angles are shared by many heads (8192 x 64 x 128 bf16: 46.0
+// us, with 2 or 9 a thread 48.0 or 47.1).  Appending wants sixteen: its tokens'
+// slots take three dependent loads, which more tokens a block go through together
+// (6001 tokens of 64 + 8 + 8 heads: 44.5 us, with four a thread 55.1).  A call that
+// then has fewer blocks than the device has SMs takes smaller blocks, each repeating
+// its tokens' angles, since it is latency that bounds it.
 constexpr long long kWantBlocks = 148;
-constexpr int kItemsPerThread = 4;
+constexpr int kRopeItems = 4, kAppendItems = 16;
 
 void block_shape(sha::RopeParams &p, bool append, int &grid_x, int &grid_y)
 {
@@ -34,7 +37,7 @@ void block_shape(sha::RopeParams &p, bool append, int &grid_x, int &grid_y)
     const int per_row = p.rotary / 2 / P + (p.d - p.rotary) / copy;
     const int heads = p.H_a + (append ? p.H_kv : 0);
     const int lanes = sha::kRopeThreads / per_row;            // rows a pass
-    int rows = lanes * kItemsPerThread;
+    int rows = lanes * (append ? kAppendItems : kRopeItems);
     while (rows > lanes && ((long long)p.T * heads + rows - 1) / rows < kWantBlocks) rows -= lanes;
     int hpb = heads < rows ? heads : rows;
     int runs = (heads + hpb - 1) / hpb;
