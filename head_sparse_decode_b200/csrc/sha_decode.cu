@@ -922,41 +922,33 @@ sha_status_t launch_prefix(const sha::PrefixParams &prm, const void *k, const vo
 {
     using C = sha::PrefixConfig<D>;
     using Suffix = sha::SuffixConfig<D>;
-    auto kernel = sha::sha_prefix_kernel<T, D>;
-    const bool tall = prm.H_q / prm.H_kv > 8;
-    auto suffix_kernel = tall ? sha::sha_suffix_kernel<T, D, 2> : sha::sha_suffix_kernel<T, D, 1>;
+    auto low = sha::sha_prefix_kernel<T, D, 1>;      // up to 8 query rows a group
+    auto tall = sha::sha_prefix_kernel<T, D, 2>;
     static std::atomic<bool> configured[kMaxDevices];
     if (!configured[dev].load(std::memory_order_acquire)) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(low, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              C::kSmemBytes);
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(sha::sha_suffix_kernel<T, D, 1>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     Suffix::kSmemBytes);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(sha::sha_suffix_kernel<T, D, 2>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     Suffix::kSmemBytes);
+            e = cudaFuncSetAttribute(tall, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     C::kSmemBytes);
         if (e != cudaSuccess) return launch_error(e);
         configured[dev].store(true, std::memory_order_release);
     }
     const int box_rows = prm.page_size < C::kTile ? prm.page_size : C::kTile;
+    const int suffix_box = prm.page_size < Suffix::kStage ? prm.page_size : Suffix::kStage;
     const long long planes = (long long)prm.num_pages * prm.H_kv;
-    CUtensorMap tm_k, tm_v;
+    CUtensorMap tm_k, tm_v, ts_k, ts_v;
     sha_status_t st = kv_tensor_map(&tm_k, k, dtype, D, prm.page_size, planes, box_rows);
     if (st == SHA_OK) st = kv_tensor_map(&tm_v, v, dtype, D, prm.page_size, planes, box_rows);
-    if (st != SHA_OK) return st;
-    cudaError_t e = launch_kernel(kernel, num_sms, C::kThreads, C::kSmemBytes, stream, prm, tm_k,
-                                  tm_v);
-    if (e != cudaSuccess) return launch_error(e);
-    const int suffix_box = prm.page_size < Suffix::kStage ? prm.page_size : Suffix::kStage;
+    ts_k = tm_k;
+    ts_v = tm_v;
     if (suffix_box != box_rows) {
-        st = kv_tensor_map(&tm_k, k, dtype, D, prm.page_size, planes, suffix_box);
-        if (st == SHA_OK) st = kv_tensor_map(&tm_v, v, dtype, D, prm.page_size, planes, suffix_box);
-        if (st != SHA_OK) return st;
+        if (st == SHA_OK) st = kv_tensor_map(&ts_k, k, dtype, D, prm.page_size, planes, suffix_box);
+        if (st == SHA_OK) st = kv_tensor_map(&ts_v, v, dtype, D, prm.page_size, planes, suffix_box);
     }
-    e = launch_kernel(suffix_kernel, num_sms, Suffix::kThreads, Suffix::kSmemBytes, stream, suffix,
-                      tm_k, tm_v);
+    if (st != SHA_OK) return st;
+    cudaError_t e = launch_kernel(prm.H_q / prm.H_kv > 8 ? tall : low, num_sms, C::kThreads,
+                                  C::kSmemBytes, stream, prm, suffix, tm_k, tm_v, ts_k, ts_v);
     if (e != cudaSuccess) return launch_error(e);
     const long long rows = (long long)prm.B * prm.top_k * (prm.H_q / prm.H_kv);
     // four warps a row while rows are few (up to four waves of resident blocks)

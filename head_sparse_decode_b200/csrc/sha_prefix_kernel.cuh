@@ -1,4 +1,4 @@
-// sha_prefix_kernel.cuh -- the shared-prefix pass of sha_decode_prefix.
+// sha_prefix_kernel.cuh -- the kernels of sha_decode_prefix.
 //
 // When every row of a batch begins with the same P keys, the attention over
 // them is, for each KV head h, one dense product: the query rows of all the
@@ -6,11 +6,16 @@
 // same K_h, V_h [P, d].  Reading the prefix once per head instead of once per
 // unit divides its traffic by R_h (about B * top_k / H_kv).  The softmax over a
 // row's whole key range is put together from its two parts by the log-sum-exp
-// rule: this kernel leaves (O, m, l) of each query row over [0, P), the suffix
-// pass (sha_suffix_kernel.cuh) those over the row's own keys, and a
-// third kernel, wide enough to keep many loads in flight, puts them together.  (Put
-// together by the suffix pass at the end of each unit they cost it 3 us a unit, its
-// ring standing full meanwhile: 113 us against 78 for the OPT-66B-shaped batch.)
+// rule: some blocks of the first kernel leave (O, m, l) of each query row over
+// [0, P), the others (sha_suffix_kernel.cuh) those over the rows' own keys, and a
+// second kernel, wide enough to keep many loads in flight, puts them together.
+// (Put together at the end of each unit they cost its block 3 us a unit, its ring
+// standing full meanwhile.)
+//
+// The two parts run side by side, not one after the other: each alone leaves the
+// memory idle while it plans, fetches its first tiles and writes its states.  How
+// many blocks take the prefix is decided on the device, by a small cost model of
+// both parts (prefix_share).
 //
 // How the work is cut.  The selection is on the device, so each block plans for
 // itself: a histogram of batch_head_index gives every head's units, 256 / G units
@@ -51,6 +56,7 @@
 
 #include "sha_device.cuh"
 #include "sha_gqa_kernel.cuh"
+#include "sha_suffix_kernel.cuh"
 #include "sha_tcgen05.cuh"
 
 namespace sha {
@@ -115,13 +121,19 @@ struct PrefixConfig {
     static constexpr int kQRowOffset = kUnitOffset + 4 * kRows;     // and the rows of q they are
     static constexpr int kStartOffset = kQRowOffset + 4 * kRows;    // first row tile of each head
     static constexpr int kPairOffset = kStartOffset + 4 * (kPrefixMaxHeads + 1);
-    static constexpr int kSmemBytes = 1024 + kPairOffset + 4 * (kPrefixMaxHeads + 1);
+    static constexpr int kPlanOffset = (kPairOffset + 4 * (kPrefixMaxHeads + 1) + 7) / 8 * 8;
+    static constexpr int kSuffixBarOffset = kPlanOffset + 16 * (kThreads / 32);
+    static constexpr int kSmemBytes =
+        1024 + kSuffixBarOffset + 8 * SuffixConfig<D>::kWorkers * SuffixConfig<D>::kStages;
     // tensor memory: S of the two streams, P, then O
     static constexpr int kTmemCols = 512;
     static constexpr int kTmemP = 2 * kStep;
     static constexpr int kTmemO = 256;
     static_assert(kTile == 2 * kStep, "two steps of a tile, one per stream or two of both");
     static_assert(kBarOffset % 8 == 0 && kCtlOffset % 4 == 0, "alignment");
+    static_assert(SuffixConfig<D>::kWorkers * SuffixConfig<D>::kRingBytes <= kBarOffset,
+                  "the workers' rings lie where the tiles and queries would");
+    static_assert(SuffixConfig<D>::kWorkers <= kThreads / 32, "a warp per worker");
     static_assert(kTmemP + kStep <= kTmemO && kTmemO + 2 * D <= kTmemCols, "S, P and O fit");
 };
 
@@ -202,6 +214,7 @@ struct PrefixCut {
     int heads;
     unsigned key_tiles;
     unsigned pieces, pieces2;    // > 0: pieces of a row tile of up to, of more than 128 rows
+    unsigned used;               // blocks with tiles
     unsigned base, extra;        // else block c has base tiles, the first `extra` one more
     unsigned t, t_end;           // this block's range
     int own_pieces;              // (pieces) those of this block's row tile
@@ -235,7 +248,7 @@ struct PrefixCut {
         pairs = pairs_;
         heads = heads_;
         key_tiles = tiles;
-        pieces = pieces2 = base = extra = t = t_end = 0;
+        pieces = pieces2 = base = extra = t = t_end = used = 0;
         const unsigned row_tiles = (unsigned)start[heads], wide = (unsigned)pairs[heads];
         const unsigned total = row_tiles * tiles;
         if (total == 0) return;
@@ -246,7 +259,8 @@ struct PrefixCut {
             const unsigned q1 = (tiles + p1 - 1) / p1, q2 = (tiles + p2 - 1) / p2;
             pieces = (tiles + q1 - 1) / q1;
             pieces2 = (tiles + q2 - 1) / q2;
-            if (block >= block_of(heads)) return;
+            used = block_of(heads);
+            if (block >= used) return;
             const int h = search(block, [&](int x) { return block_of(x); });
             unsigned k = block - block_of(h);
             const unsigned wide_tiles = (unsigned)(pairs[h + 1] - pairs[h]);
@@ -263,6 +277,7 @@ struct PrefixCut {
             return;
         }
         const unsigned blocks = min(total, grid);
+        used = blocks;
         const unsigned even = (total + blocks - 1) / blocks + 2 * kRunTiles;
         const unsigned whole = (row_tiles + blocks - 1) / blocks;
         if (whole * (tiles + kRunTiles) <= even) {
@@ -301,6 +316,45 @@ struct PrefixCut {
     }
 };
 
+// How many of the call's `blocks` blocks the prefix may take: the number at which
+// the slower of the two parts is done first, out of 32 evenly spaced ones, one per
+// lane of the calling warp.  Times in ns, measured: a run's beginning and end; a key
+// tile of 128 keys by up to 128 rows, and by more; a worker's beginning; an SM's
+// share of a weight of the suffix (32 keys' bytes, per 64 elements of d).
+constexpr float kPrefixRunNs = 8000.f, kPrefixTileNs = 1500.f, kPrefixWideNs = 2450.f;
+constexpr float kSuffixRunNs = 5000.f, kSuffixWeightNs = 80.f;
+__device__ __forceinline__ int prefix_share(int row_tiles, int wide, int tiles, long long weights,
+                                            int d64, int blocks)
+{
+    const int lane = threadIdx.x & 31;
+    const int share = max(1, min(blocks - 1, (lane + 1) * blocks / 33));
+    const int weight = row_tiles + wide;
+    float t;
+    if (weight <= share) {
+        const int p1 = min(share / weight, tiles), p2 = min(2 * share / weight, tiles);
+        t = fmaxf(row_tiles > wide ? (float)((tiles + p1 - 1) / p1) * kPrefixTileNs : 0.f,
+                  wide > 0 ? (float)((tiles + p2 - 1) / p2) * kPrefixWideNs : 0.f) +
+            kPrefixRunNs;
+    } else {
+        t = ((float)(row_tiles - wide) * kPrefixTileNs + (float)wide * kPrefixWideNs) *
+                (float)tiles / (float)share +
+            (float)((row_tiles + share - 1) / share) * kPrefixRunNs;
+    }
+    t = fmaxf(t, kSuffixRunNs +
+                     (float)weights * (kSuffixWeightNs * (float)d64) / (float)(blocks - share));
+    int best = share;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        const float x = __shfl_xor_sync(0xffffffffu, t, off);
+        const int y = __shfl_xor_sync(0xffffffffu, best, off);
+        if (x < t || (x == t && y < best)) {
+            t = x;
+            best = y;
+        }
+    }
+    return best;
+}
+
 // Ring position of a run's K and V tiles: K_0, then K_i, V_(i-1) for i = 1 .. n-1,
 // then V_(n-1) -- the order in which the products use them.
 __device__ __forceinline__ int prefix_k_pos(int i) { return i == 0 ? 0 : 2 * i - 1; }
@@ -332,13 +386,18 @@ struct PrefixSteps {
     __device__ __forceinline__ bool takes_last(int st) const { return pair || st < last_halves; }
 };
 
-template <typename T, int D>
+// kNT: see suffix_worker.  tm_k, tm_v: boxes of up to 128 keys; ts_k, ts_v: of up to 32.
+template <typename T, int D, int kNT>
 __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
-    sha_prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_k,
-                      const __grid_constant__ CUtensorMap tm_v)
+    sha_prefix_kernel(const PrefixParams p, const SuffixParams suffix,
+                      const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v,
+                      const __grid_constant__ CUtensorMap ts_k,
+                      const __grid_constant__ CUtensorMap ts_v)
 {
     using C = PrefixConfig<D>;
     using Tile = typename C::Tile;
+    using Suffix = SuffixConfig<D>;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr uint32_t kIdescS = umma_idesc_f16(kBf16, 128, C::kStep);
     constexpr uint32_t kIdescO = umma_idesc_f16(kBf16, 128, D, false, true);
@@ -382,8 +441,40 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
             mbar_init(&drain[s], 1);
         }
         *abort_flag = 0;
+        uint64_t *own = reinterpret_cast<uint64_t *>(smem + C::kSuffixBarOffset);
+        for (int s = 0; s < Suffix::kWorkers * Suffix::kStages; ++s) mbar_init(&own[s], 1);
         mbar_init_fence();
     }
+    pdl_wait();
+    pdl_launch_dependents();
+
+    // the two parts' work, and who does what
+    long long *plan = reinterpret_cast<long long *>(smem + C::kPlanOffset);
+    suffix_totals<D, C::kThreads>(suffix, plan);
+    prefix_row_tiles<C::kThreads>(p, G, units_per_tile, start, pairs);
+    const int key_tiles = (p.keys + C::kTile - 1) / C::kTile;
+    long long weights;
+    int longest;
+    suffix_read_totals<C::kThreads>(plan, weights, longest);
+    const int share = prefix_share(start[p.H_kv], pairs[p.H_kv], key_tiles, weights, D / 64,
+                                   (int)gridDim.x);
+    PrefixCut wk;
+    wk.plan(start, pairs, p.H_kv, (unsigned)key_tiles, (unsigned)share, blockIdx.x);
+    if (blockIdx.x >= wk.used) {
+        // ------------------------------------------------------------ rows' own keys
+        if (warp >= Suffix::kWorkers) return;
+        const int blocks = (int)(gridDim.x - wk.used);
+        // neighbouring workers on different SMs, so that a small call uses them all
+        const int worker = warp * blocks + (int)(blockIdx.x - wk.used);
+        SuffixWalk walk;
+        if (suffix_plan<D>(suffix, weights, longest, blocks * Suffix::kWorkers, worker, walk))
+            suffix_worker<T, D, kNT>(
+                suffix, ts_k, ts_v, walk, worker, smem + warp * Suffix::kRingBytes,
+                reinterpret_cast<uint64_t *>(smem + C::kSuffixBarOffset) + warp * Suffix::kStages,
+                abort_flag);
+        return;
+    }
+    // ---------------------------------------------------------------- the shared keys
     if (warp == 1) {
         tmem_alloc(reinterpret_cast<uint32_t *>(smem + C::kCtlOffset) + 2, C::kTmemCols);
         tmem_relinquish();
@@ -392,13 +483,6 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = (uint32_t)ctl[2];
-    pdl_wait();
-    pdl_launch_dependents();
-
-    prefix_row_tiles<C::kThreads>(p, G, units_per_tile, start, pairs);
-    PrefixCut wk;
-    wk.plan(start, pairs, p.H_kv, (unsigned)((p.keys + C::kTile - 1) / C::kTile), gridDim.x,
-            blockIdx.x);
     PrefixRun run;
 
     // waits give up together: the first that runs out raises the abort flag
@@ -833,7 +917,7 @@ __global__ void __launch_bounds__(kMergeThreads) sha_prefix_merge_kernel(const P
     const int local = warp / kWays * kRowsPerWarp + (threadIdx.x & 31) / kLanes;
     const long long rows = (long long)p.B * p.top_k * G;
     const long long at = (long long)blockIdx.x * kRowsPerBlock + local;
-    // (the call's inputs were complete before the passes began)
+    // (the call's inputs were complete before the first kernel's blocks began)
     const bool inside = at < rows;
     const int u = inside ? (int)(at / G) : 0, j = inside ? (int)(at - (long long)u * G) : 0;
     const int b = u / p.top_k, h = p.idx[u], len = p.seqlens[b];

@@ -1,4 +1,5 @@
-// sha_suffix_kernel.cuh -- the rows' own keys in sha_decode_prefix: for each
+// sha_suffix_kernel.cuh -- the rows' own keys in sha_decode_prefix, the part of its
+// blocks that do not work on the prefix (sha_prefix_kernel.cuh): for each
 // selected (batch row, slot) unit the attention of its G query rows over keys
 // [P, len) of the row's pages, left as partial states (O, m, l) for the merge.
 //
@@ -10,7 +11,7 @@
 // the time its bytes take.  Here every warp is a worker of its own: it has its own
 // ring of key stages in shared memory, issues its own TMA loads, keeps its own
 // softmax state in registers and writes it out itself, with no barrier between
-// warps.  The workers of an SM (6 at d = 128, 12 at d = 64) hide one another's
+// warps.  The workers of an SM (6 at d = 128, 10 at d = 64) hide one another's
 // latencies, and their rings (2 stages of 32 keys) together keep 190 KiB in flight.
 //
 // How, for a stage of 32 keys.  The products are turned over, keys and head
@@ -51,18 +52,13 @@ struct SuffixParams {
 
 template <int D>
 struct SuffixConfig {
-    static constexpr int kWorkers = D == 128 ? 6 : 12;
-    static constexpr int kThreads = 32 * kWorkers;
+    static constexpr int kWorkers = D == 128 ? 6 : 10;   // warps of the block at work
     static constexpr int kStage = 32;                    // keys
     static constexpr int kStages = 2;
     static constexpr int kBoxes = D / 64;
     static constexpr int kBoxBytes = kStage * 128;
     static constexpr int kTileBytes = kBoxes * kBoxBytes;        // K or V of a stage
     static constexpr int kRingBytes = kStages * 2 * kTileBytes;
-    static constexpr int kBarOffset = kWorkers * kRingBytes;
-    static constexpr int kPlanOffset = kBarOffset + 8 * kWorkers * kStages;
-    static constexpr int kFlagOffset = kPlanOffset + 16 * kWorkers;
-    static constexpr int kSmemBytes = 1024 + kFlagOffset + 16;
     // a unit's latency in stages: with 6 workers an SM streams a 32-key stage in
     // 0.37 us, and a unit costs a worker about 4 us, 0.7 us of the SM
     static constexpr int kUnitCost = 2;
@@ -146,18 +142,18 @@ struct SuffixWalk {
     }
 };
 
-// The calling warp's walk: false if it has nothing to do.  All threads of the
-// block call it (it synchronises with __syncthreads).
-template <int D>
-__device__ __forceinline__ bool suffix_plan(const SuffixParams &p, long long *scratch, int worker,
-                                            SuffixWalk &w)
+// The weights of all units and the longest row's stages.  All NT threads of the
+// block; scratch: shared, 2 * NT / 32 longs.  The caller synchronises before and
+// after; `sum` and `longest` come from the scratch by suffix_read_totals.
+template <int D, int NT>
+__device__ __forceinline__ void suffix_totals(const SuffixParams &p, long long *scratch)
 {
     using C = SuffixConfig<D>;
     const unsigned FULL = 0xffffffffu;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     long long sum = 0;
     int tmax = 0;
-    for (int r = tid; r < p.B; r += C::kThreads) {
+    for (int r = tid; r < p.B; r += NT) {
         const int T = suffix_stages(p, p.seqlens[r], C::kStage);
         if (T == 0) {
             if (blockIdx.x == 0) atomicOr(&g_sha_status, kStatusBadIndex);
@@ -175,19 +171,34 @@ __device__ __forceinline__ bool suffix_plan(const SuffixParams &p, long long *sc
         scratch[2 * warp] = sum;
         scratch[2 * warp + 1] = tmax;
     }
-    __syncthreads();
-    long long total = 0;
-    tmax = 0;
-    for (int i = 0; i < C::kWorkers; ++i) {
-        total += scratch[2 * i];
-        tmax = max(tmax, (int)scratch[2 * i + 1]);
+}
+template <int NT>
+__device__ __forceinline__ void suffix_read_totals(const long long *scratch, long long &sum,
+                                                   int &longest)
+{
+    sum = 0;
+    longest = 0;
+#pragma unroll
+    for (int i = 0; i < NT / 32; ++i) {
+        sum += scratch[2 * i];
+        longest = max(longest, (int)scratch[2 * i + 1]);
     }
+}
+
+// The walk of worker `worker` of all `all` (a whole warp calls it together): false if
+// it has nothing to do.
+template <int D>
+__device__ __forceinline__ bool suffix_plan(const SuffixParams &p, long long total, int longest,
+                                            int all, int worker, SuffixWalk &w)
+{
+    using C = SuffixConfig<D>;
+    const unsigned FULL = 0xffffffffu;
+    const int lane = threadIdx.x & 31;
     if (total == 0) return false;
     // workers in use: each with kMinWeight at least, and no unit in many more than
     // kMaxRuns pieces
-    long long least = (tmax + C::kMaxRuns - 1) / C::kMaxRuns;
+    long long least = (longest + C::kMaxRuns - 1) / C::kMaxRuns;
     if (least < C::kMinWeight) least = C::kMinWeight;
-    const int all = (int)gridDim.x * C::kWorkers;
     const int n = total >= all * least ? all : total < least ? 1 : (int)div_small(total, least);
     if (worker >= n) return false;
     w.base = div_small(total, n);
@@ -233,40 +244,19 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x)
     return y;
 }
 
-// kNT: 8-row tiles of query rows (1 for G <= 8, else 2).
+// One worker (a warp) of a block.  kNT: 8-row tiles of query rows (1 for G <= 8, else
+// 2).  ring: this worker's, 1 KiB aligned; full: its kStages barriers, initialised.
 template <typename T, int D, int kNT>
-__global__ void __launch_bounds__(SuffixConfig<D>::kThreads, 1)
-    sha_suffix_kernel(const SuffixParams p, const __grid_constant__ CUtensorMap tm_k,
-                      const __grid_constant__ CUtensorMap tm_v)
+__device__ __forceinline__ void suffix_worker(const SuffixParams &p, const CUtensorMap &tm_k,
+                                              const CUtensorMap &tm_v, SuffixWalk walk, int worker,
+                                              unsigned char *ring, uint64_t *full,
+                                              volatile int *abort_flag)
 {
     using C = SuffixConfig<D>;
     constexpr int kKT = C::kStage / 16;                 // 16-key tiles of a stage
-    extern __shared__ __align__(1024) unsigned char smem_raw[];
-    unsigned char *smem = reinterpret_cast<unsigned char *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31;
     const unsigned FULL = 0xffffffffu;
     const int G = p.H_q / p.H_kv;
-    // neighbouring workers on different SMs, so that a small call uses them all
-    const int worker = warp * (int)gridDim.x + (int)blockIdx.x;
-    unsigned char *ring = smem + warp * C::kRingBytes;
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBarOffset) + warp * C::kStages;
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kFlagOffset);
-
-    if (lane < C::kStages) mbar_init(&full[lane], 1);
-    if (threadIdx.x == 0) *abort_flag = 0;
-    mbar_init_fence();
-    // The kernel before this one is the prefix pass of the same call: it lets this
-    // one start only after everything before it has finished, and nothing that it
-    // writes is read or overwritten here, so it is only waited for at the end.
-    pdl_launch_dependents();
-    SuffixWalk walk;
-    const bool any =
-        suffix_plan<D>(p, reinterpret_cast<long long *>(smem + C::kPlanOffset), worker, walk);
-    if (!any) {
-        pdl_wait();
-        return;
-    }
 
     // ---- the loads: stage by stage through this worker's runs, ahead of the use
     const uint64_t policy = l2_policy_evict_first();
@@ -515,8 +505,6 @@ __global__ void __launch_bounds__(SuffixConfig<D>::kThreads, 1)
     for (; used < issued; ++used)
         if (lane == 0) mbar_wait_drain(&full[used % C::kStages], (used / C::kStages) & 1);
     __syncwarp();
-    // the prefix pass before this one has finished, too, when this one has
-    pdl_wait();
 }
 
 }  // namespace sha
