@@ -502,47 +502,57 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
         // every call reads the prefix again: the L2's default policy may keep it
         uint64_t policy;
         asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
-        uint32_t used = 0, last_parity = 0;
-        uint32_t base = 0;
-        bool ok = true;
+        uint32_t used = 0, last_parity = 0, pos = 0;
         const int box_rows = min(p.page_size, C::kTile);
-        while (ok && wk.next(run)) {
-            const int h = run.head;
-            const int n = run.n;
-            for (int i = 0; ok && i < 2 * n; ++i) {
-                // position i is K_0, K_((i+1)/2) (odd i < 2n-1) or V
-                const bool is_k = i == 0 || ((i & 1) && i < 2 * n - 1);
-                const int jj = is_k ? (i + 1) / 2 : (i == 2 * n - 1 ? n - 1 : i / 2 - 1);
-                const int buf = (int)((base + (uint32_t)i) % C::kBufs);
-                const uint32_t parity = ((base + (uint32_t)i) / C::kBufs) & 1u;
-                if (lane == 0) ok = wait(&empty[buf], parity ^ 1);
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (!ok) break;
-                const int n0 = (run.first + jj) * C::kTile;
-                const int rows = min(C::kTile, p.keys - n0);
-                const int chunks = (rows + box_rows - 1) / box_rows;
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&full[buf],
-                                          (uint32_t)(chunks * Tile::kBoxes * box_rows * 128));
-                __syncwarp();
-                unsigned char *dst = smem + buf * C::kTileBytes;
-                for (int c = lane; c < chunks; c += 32) {
-                    const int key = n0 + c * box_rows;
-                    const int pi = key / p.page_size, off = key - pi * p.page_size;
-                    int page = p.table[pi];
-                    if ((unsigned)page >= (unsigned)p.num_pages) {
-                        atomicOr(&g_sha_status, kStatusBadIndex);
-                        page = 0;                       // stay inside the pool
-                    }
-                    for (int bx = 0; bx < Tile::kBoxes; ++bx)
-                        tma_load_3d(dst + bx * Tile::kBoxBytes + c * box_rows * 128,
-                                    is_k ? &tm_k : &tm_v, bx * 64, off, page * p.H_kv + h,
-                                    &full[buf], policy);
+        // a tile's pages, one box per lane (at most 16), looked up a tile ahead of its K
+        auto rows_of = [&](int tile) { return min(C::kTile, p.keys - tile * C::kTile); };
+        auto pages_of = [&](int tile) {
+            return lane * box_rows < rows_of(tile)
+                       ? p.table[(tile * C::kTile + lane * box_rows) / p.page_size]
+                       : 0;
+        };
+        auto load = [&](int tile, int page, int h, const CUtensorMap *map) {
+            const int buf = (int)(pos % C::kBufs);
+            const uint32_t parity = (pos / C::kBufs) & 1u;
+            ++pos;
+            bool ok = true;
+            if (lane == 0) ok = wait(&empty[buf], parity ^ 1);
+            if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
+            const int rows = rows_of(tile);
+            const int chunks = (rows + box_rows - 1) / box_rows;
+            if (lane == 0)
+                mbar_arrive_expect_tx(&full[buf], (uint32_t)(chunks * Tile::kBoxes * box_rows * 128));
+            __syncwarp();
+            if (lane < chunks) {
+                if ((unsigned)page >= (unsigned)p.num_pages) {
+                    atomicOr(&g_sha_status, kStatusBadIndex);
+                    page = 0;                           // stay inside the pool
                 }
-                last_parity = (last_parity & ~(1u << buf)) | (parity << buf);
-                used |= 1u << buf;
+                const int off = (tile * C::kTile + lane * box_rows) % p.page_size;
+                unsigned char *dst = smem + buf * C::kTileBytes + lane * box_rows * 128;
+#pragma unroll
+                for (int bx = 0; bx < Tile::kBoxes; ++bx)
+                    tma_load_3d(dst + bx * Tile::kBoxBytes, map, bx * 64, off, page * p.H_kv + h,
+                                &full[buf], policy);
             }
-            base += 2 * n;
+            last_parity = (last_parity & ~(1u << buf)) | (parity << buf);
+            used |= 1u << buf;
+            return true;
+        };
+        bool ok = true;
+        while (ok && wk.next(run)) {
+            // K_0, then K_i, V_(i-1), then the last V: the order of prefix_k_pos
+            int page = pages_of(run.first), next = 0;
+            if (run.n > 1) next = pages_of(run.first + 1);
+            ok = load(run.first, page, run.head, &tm_k);
+            for (int i = 1; ok && i < run.n; ++i) {
+                const int tile = run.first + i;
+                const int after = i + 1 < run.n ? pages_of(tile + 1) : 0;
+                ok = load(tile, next, run.head, &tm_k) && load(tile - 1, page, run.head, &tm_v);
+                page = next;
+                next = after;
+            }
+            ok = ok && load(run.first + run.n - 1, page, run.head, &tm_v);
         }
         if (lane == 0)
             for (int s = 0; s < C::kBufs; ++s)
