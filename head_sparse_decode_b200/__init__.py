@@ -319,8 +319,8 @@ def sha_decode_prefix(q, k_pages, v_pages, batch_head_index, seqlens, block_tabl
     if workspace is None:
         nbytes = _prefix_workspace_size(B, H_q, H_kv, d, top_k, index)
         workspace = seqlens.new_empty((nbytes + 3) // 4)
-        if stream is not None and handle != torch._C._cuda_getCurrentRawStream(index):
-            workspace.record_stream(torch.cuda.ExternalStream(handle, device=dev))
+        if stream is not None:
+            _record_on(workspace, stream, dev)
     else:
         if workspace.get_device() != index or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {dev}")
@@ -641,6 +641,14 @@ def _raw_stream(stream, device):
     return _stream_handle(stream, device)
 
 
+def _record_on(t, stream, device):
+    """Keep t's memory until `stream` is done with it, where that is not the stream t was
+    allocated on."""
+    handle = _stream_handle(stream, device)
+    if handle != torch._C._cuda_getCurrentRawStream(device.index):
+        t.record_stream(torch.cuda.ExternalStream(handle, device=device))
+
+
 def _on_device(device, entry, args):
     """entry(*args) with `device` current; raises on an error status.  The device is
     switched only if it is not the current one already."""
@@ -878,6 +886,39 @@ def _explain_append(k, v, k_pages, v_pages, block_table, positions, rows, inv_fr
         _check_contiguous("inv_freq", inv_freq, 1, torch.float64, index)
 
 
+def append_decode_paged(q, k, v, k_pages, v_pages, batch_head_index, positions, seqlens,
+                        block_table, inv_freq=None, interleaved=False, mscale=1.0, prefix_len=0,
+                        prefix_table=None, scale=None, out=None, workspace=None, stream=None):
+    """One decode step of a layer over a paged cache, on one stream: each row's new key
+    and value are appended at positions[b] (with inv_freq rotated, and the queries with
+    them), then the selected heads attend to keys [0, seqlens[b]) -- seqlens counts the
+    new key, so it is positions + 1.  With prefix_len > 0 the rows share the prefix in
+    prefix_table's pages (sha_decode_prefix), else sha_decode_paged runs.
+
+    q [B, H_q, d] and k, v [B, H_kv, d] are views with d contiguous (slices of a fused
+    projection's rows); out [B, H_q, d] is new if not given, its unselected rows then
+    uninitialised.  Without inv_freq q must be contiguous."""
+    if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+        raise ValueError("q must be [B, H_q, d] and k [B, H_kv, d]")
+    if inv_freq is None:
+        sha_append_paged(k, v, k_pages, v_pages, block_table, positions, stream=stream)
+        turned = q
+    else:
+        turned = torch.empty_like(q, memory_format=torch.contiguous_format)
+        if stream is not None and q.is_cuda:
+            _record_on(turned, stream, q.device)
+        sha_append_paged(k, v, k_pages, v_pages, block_table, positions, inv_freq=inv_freq,
+                         interleaved=interleaved, mscale=mscale, q=q, q_out=turned, stream=stream)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if prefix_len > 0:
+        return sha_decode_prefix(turned, k_pages, v_pages, batch_head_index, seqlens, block_table,
+                                 prefix_len, prefix_table, scale, out, workspace=workspace,
+                                 stream=stream)
+    return sha_decode_paged(turned, k_pages, v_pages, batch_head_index, seqlens, block_table, scale,
+                            out, stream=stream)
+
+
 def sha_get_device_status(stream=None, device=None):
     """Synchronise ``stream`` and read-and-clear the device's sticky flags; returns a
     status code (SHA_OK, SHA_ERR_BAD_INDEX or SHA_ERR_TIMEOUT)."""
@@ -905,5 +946,5 @@ __all__ = [
     "sha_copy_bandwidth_probe", "decode",
     "alloc_workspace", "ShaError", "LIBRARY_PATH", "sha_decode_noalloc",
     "rope_frequencies", "sha_rope", "sha_append_paged", "sha_decode_prefix",
-    "sha_decode_prefix_workspace_size",
+    "sha_decode_prefix_workspace_size", "append_decode_paged",
 ]

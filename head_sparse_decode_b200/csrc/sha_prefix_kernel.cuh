@@ -255,22 +255,23 @@ struct PrefixCut {
         const unsigned weight = row_tiles + wide;
         if (weight <= grid) {
             // the longest piece of each kind, then as few pieces as keep to it
-            const unsigned p1 = min(grid / weight, tiles), p2 = min(2 * grid / weight, tiles);
-            const unsigned q1 = (tiles + p1 - 1) / p1, q2 = (tiles + p2 - 1) / p2;
-            pieces = (tiles + q1 - 1) / q1;
-            pieces2 = (tiles + q2 - 1) / q2;
+            const unsigned p1 = min(div_fast(grid, weight), tiles);
+            const unsigned p2 = min(div_fast(2 * grid, weight), tiles);
+            const unsigned q1 = div_fast(tiles + p1 - 1, p1), q2 = div_fast(tiles + p2 - 1, p2);
+            pieces = div_fast(tiles + q1 - 1, q1);
+            pieces2 = div_fast(tiles + q2 - 1, q2);
             used = block_of(heads);
             if (block >= used) return;
             const int h = search(block, [&](int x) { return block_of(x); });
             unsigned k = block - block_of(h);
             const unsigned wide_tiles = (unsigned)(pairs[h + 1] - pairs[h]);
-            unsigned r = k / pieces2, own = pieces2;
+            unsigned r = div_fast(k, pieces2), own = pieces2;
             if (r >= wide_tiles) {               // the last row tile, of up to 128 rows
                 r = wide_tiles;
                 own = pieces;
             }
             k -= r * pieces2;
-            const unsigned b = tiles / own, x = tiles - b * own;
+            const unsigned b = div_fast(tiles, own), x = tiles - b * own;
             t = ((unsigned)start[h] + r) * tiles + k * b + min(k, x);
             t_end = t + b + (k < x);
             own_pieces = (int)own;
@@ -296,7 +297,7 @@ struct PrefixCut {
     __device__ __forceinline__ bool next(PrefixRun &r)
     {
         if (t >= t_end) return false;
-        r.row_tile = (int)(t / key_tiles);
+        r.row_tile = (int)div_fast(t, key_tiles);
         r.head = search((unsigned)r.row_tile, [&](int x) { return (unsigned)start[x]; });
         const unsigned end = ((unsigned)r.row_tile + 1) * key_tiles;
         r.first = (int)(t - (unsigned)r.row_tile * key_tiles);
@@ -330,18 +331,21 @@ __device__ __forceinline__ int prefix_share(int row_tiles, int wide, int tiles, 
     const int share = max(1, min(blocks - 1, (lane + 1) * blocks / 33));
     const int weight = row_tiles + wide;
     float t;
+    // (an estimate: in floats, the divisions approximate)
+    const float f = (float)tiles;
     if (weight <= share) {
-        const int p1 = min(share / weight, tiles), p2 = min(2 * share / weight, tiles);
-        t = fmaxf(row_tiles > wide ? (float)((tiles + p1 - 1) / p1) * kPrefixTileNs : 0.f,
-                  wide > 0 ? (float)((tiles + p2 - 1) / p2) * kPrefixWideNs : 0.f) +
+        const float per = __fdividef((float)share + 0.5f, (float)weight);
+        const float p1 = fminf(floorf(per), f), p2 = fminf(floorf(2.f * per), f);
+        t = fmaxf(row_tiles > wide ? ceilf(__fdividef(f, p1) - 1e-3f) * kPrefixTileNs : 0.f,
+                  wide > 0 ? ceilf(__fdividef(f, p2) - 1e-3f) * kPrefixWideNs : 0.f) +
             kPrefixRunNs;
     } else {
-        t = ((float)(row_tiles - wide) * kPrefixTileNs + (float)wide * kPrefixWideNs) *
-                (float)tiles / (float)share +
-            (float)((row_tiles + share - 1) / share) * kPrefixRunNs;
+        const float each = __fdividef(1.f, (float)share);
+        t = ((float)(row_tiles - wide) * kPrefixTileNs + (float)wide * kPrefixWideNs) * f * each +
+            ceilf((float)row_tiles * each) * kPrefixRunNs;
     }
     t = fmaxf(t, kSuffixRunNs +
-                     (float)weights * (kSuffixWeightNs * (float)d64) / (float)(blocks - share));
+                     __fdividef((float)weights * (kSuffixWeightNs * (float)d64), (float)(blocks - share)));
     int best = share;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
@@ -970,6 +974,16 @@ __global__ void __launch_bounds__(kMergeThreads) sha_prefix_merge_kernel(const P
             m = ml.x;
             l = ml.y;
         }
+        // the first parts' O on the way beside all (m, l), before their weights are known
+        constexpr int kAhead = 4;
+        float4 ahead[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const float *ok = reinterpret_cast<const float *>(__shfl_sync(
+                FULL, reinterpret_cast<unsigned long long>(o), k, kLanes));
+            ahead[k] = ok ? __ldcg(reinterpret_cast<const float4 *>(ok + 4 * sub))
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
         float top = m;
 #pragma unroll
         for (int off = kLanes / 2; off > 0; off >>= 1)
@@ -989,12 +1003,22 @@ __global__ void __launch_bounds__(kMergeThreads) sha_prefix_merge_kernel(const P
         O.w *= a;
         int parts = min(mine - r * kLanes, kLanes);
         if (kLanes < 32) parts = max(parts, __shfl_xor_sync(FULL, parts, 16));
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const float wk = __shfl_sync(FULL, w, k, kLanes);
+            if (wk != 0.f) {                     // (no keys, or nothing left of them)
+                O.x = fmaf(wk, ahead[k].x, O.x);
+                O.y = fmaf(wk, ahead[k].y, O.y);
+                O.z = fmaf(wk, ahead[k].z, O.z);
+                O.w = fmaf(wk, ahead[k].w, O.w);
+            }
+        }
 #pragma unroll 8
-        for (int k = 0; k < parts; ++k) {
+        for (int k = kAhead; k < parts; ++k) {
             const float wk = __shfl_sync(FULL, w, k, kLanes);
             const float *ok = reinterpret_cast<const float *>(__shfl_sync(
                 FULL, reinterpret_cast<unsigned long long>(o), k, kLanes));
-            if (wk != 0.f) {                     // (no keys, or nothing left of them)
+            if (wk != 0.f) {
                 const float4 x = __ldcg(reinterpret_cast<const float4 *>(ok + 4 * sub));
                 O.x = fmaf(wk, x.x, O.x);
                 O.y = fmaf(wk, x.y, O.y);

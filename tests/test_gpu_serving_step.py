@@ -1,0 +1,214 @@
+"""The serving operators as they are used together: decode steps that append, rotate and attend
+over a paged cache (append_decode_paged), with and without a shared prefix, against the same
+steps in 64 bits; and their pipeline waits giving up."""
+import math
+import os
+import subprocess
+import sys
+import textwrap
+
+import pytest
+import torch
+
+import rope_reference as rope
+from prefix_reference import HALF_STEP
+
+pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def sha():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import head_sparse_decode_b200 as h
+    return h
+
+
+class Steps:
+    """B rows behind a prompt of `prefix` keys in shared pages, `steps` tokens decoded for each."""
+
+    def __init__(self, B, H_q, H_kv, d, top_k, prefix, steps, page_size, dtype, seed):
+        g = torch.Generator().manual_seed(seed)
+        self.B, self.H_q, self.H_kv, self.d, self.G = B, H_q, H_kv, d, H_q // H_kv
+        self.prefix, self.steps, self.page_size, self.dtype = prefix, steps, page_size, dtype
+        # quarter turns: a rotation that swaps and negates, so that rounding it changes nothing
+        # and the decode's own bound holds for the whole step
+        self.freq = (torch.arange(d // 2) % 4).double() * (math.pi / 2)
+        self.prompt = [torch.randn((prefix, H_kv, d), generator=g).to(dtype) for _ in range(2)]
+        self.fused = torch.randn((steps, B, H_q + 2 * H_kv, d), generator=g).to(dtype)
+        first, shared = prefix // page_size, -(-prefix // page_size)
+        pages = -(-(prefix + steps) // page_size)
+        n = shared + B * (pages - first) + 2
+        perm = torch.randperm(n, generator=g).to(torch.int32)
+        self.prefix_table = perm[:shared].contiguous()
+        self.table = torch.cat([self.prefix_table[:first].expand(B, first),
+                                perm[shared:shared + B * (pages - first)].reshape(B, -1)], dim=1)
+        self.table = self.table.contiguous()
+        self.k_pages = torch.full((n, H_kv, page_size, d), float("nan"), dtype=dtype)
+        self.v_pages = self.k_pages.clone()
+        self.idx = [torch.rand((B, H_kv), generator=g).argsort(dim=1)[:, :top_k]
+                    .to(torch.int32).contiguous() for _ in range(steps)]
+
+    def split(self, t):
+        return self.fused[t].split([self.H_q, self.H_kv, self.H_kv], dim=1)
+
+    def run(self, sha, shared, stream=None):
+        """Prefill, then the steps; the outputs of every step (rows not selected are 9)."""
+        dev = "cuda"
+        kp, vp = self.k_pages.to(dev), self.v_pages.to(dev)
+        table, pt, freq = self.table.to(dev), self.prefix_table.to(dev), self.freq.to(dev)
+        pos = torch.arange(self.prefix, dtype=torch.int32, device=dev)
+        row = torch.zeros(self.prefix, dtype=torch.int32, device=dev)
+        k, v = (x.to(dev) for x in self.prompt)
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        sha.sha_append_paged(k, v, kp, vp, pt[None].contiguous(), pos, rows=row, inv_freq=freq,
+                             stream=stream)
+        if not shared or self.prefix % self.page_size:
+            # without sharing every row's first pages hold the prompt; with it only the last
+            # shared page's keys have a copy in each row's own page, and it is not read
+            for b in range(self.B if not shared else 0):
+                sha.sha_append_paged(k, v, kp, vp, table, pos, rows=row + b, inv_freq=freq)
+        outs = []
+        for t in range(self.steps):
+            q, k, v = (x.to(dev) for x in self.split(t))
+            at = torch.full((self.B,), self.prefix + t, dtype=torch.int32, device=dev)
+            out = torch.full((self.B, self.H_q, self.d), 9.0, dtype=self.dtype, device=dev)
+            if stream is not None:
+                stream.wait_stream(torch.cuda.current_stream())
+            got = sha.append_decode_paged(q, k, v, kp, vp, self.idx[t].to(dev), at, at + 1, table,
+                                          inv_freq=freq, prefix_len=self.prefix if shared else 0,
+                                          prefix_table=pt if shared else None,
+                                          scale=self.d ** -0.5, out=out, stream=stream)
+            assert got is out
+            if stream is not None:
+                stream.synchronize()
+            outs.append(out.cpu())
+        assert sha.sha_get_device_status() == sha.SHA_OK
+        return outs
+
+    def check(self, outs):
+        """The bound is that of the decode (prefix_reference)."""
+        u = HALF_STEP[self.dtype]
+        at = torch.arange(self.prefix + self.steps)
+        keys = torch.cat([self.prompt[0][:, None].expand(-1, self.B, -1, -1),
+                          torch.stack([self.split(t)[1] for t in range(self.steps)])])
+        vals = torch.cat([self.prompt[1][:, None].expand(-1, self.B, -1, -1),
+                          torch.stack([self.split(t)[2] for t in range(self.steps)])])
+        for t, out in enumerate(outs):
+            n = self.prefix + t + 1
+            q = self.split(t)[0]
+            want = torch.full(out.shape, 9.0, dtype=torch.float64)
+            bound = torch.zeros_like(want)
+            for b in range(self.B):
+                k = rope.rotate(keys[:n, b], at[:n], self.freq).to(self.dtype).double()
+                v = vals[:n, b].double()
+                qr = rope.rotate(q[b][None], at[n - 1:n], self.freq)[0].to(self.dtype).double()
+                for h in self.idx[t][b].tolist():
+                    qh = qr[h * self.G:(h + 1) * self.G]
+                    w = torch.softmax(qh @ k[:, h].T * self.d ** -0.5, dim=1)
+                    o, A = w @ v[:, h], w @ v[:, h].abs()
+                    S = self.d ** -0.5 * (qh.abs() @ k[:, h].abs().T).max()
+                    want[b, h * self.G:(h + 1) * self.G] = o
+                    bound[b, h * self.G:(h + 1) * self.G] = \
+                        u * (o.abs() + A) + n * 2.0 ** -25 * v[:, h].abs().max() \
+                        + A * (2 * (self.d + 2) * 2.0 ** -23 * S + 2.0 ** -20 + n * 2.0 ** -23)
+            excess = (out.double() - want).abs() - bound
+            assert excess.max() <= 0, f"step {t}: {float(excess.max())} over the bound"
+
+
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("B,H_q,H_kv,d,top_k,prefix,page_size,dtype", [
+    (3, 8, 2, 64, 1, 37, 8, torch.bfloat16), (5, 6, 6, 128, 4, 64, 16, torch.float16),
+    (2, 32, 2, 128, 2, 130, 64, torch.bfloat16)])
+def test_decode_steps(sha, B, H_q, H_kv, d, top_k, prefix, page_size, dtype, shared):
+    s = Steps(B, H_q, H_kv, d, top_k, prefix, 11, page_size, dtype, seed=B + prefix)
+    s.check(s.run(sha, shared))
+
+
+def test_decode_steps_on_another_stream(sha):
+    s = Steps(4, 8, 4, 64, 2, 50, 6, 16, torch.float16, seed=7)
+    first = s.run(sha, True)
+    other = s.run(sha, True, stream=torch.cuda.Stream())
+    assert all(torch.equal(a, b) for a, b in zip(first, other))
+
+
+def test_captured_step(sha):
+    """A step captured once and replayed for each token: positions and lengths move on the device."""
+    s = Steps(3, 8, 2, 128, 1, 40, 9, 8, torch.bfloat16, seed=8)
+    want = s.run(sha, True)
+    dev = "cuda"
+    kp, vp = s.k_pages.to(dev), s.v_pages.to(dev)
+    table, pt, freq = s.table.to(dev), s.prefix_table.to(dev), s.freq.to(dev)
+    sha.sha_append_paged(s.prompt[0].to(dev), s.prompt[1].to(dev), kp, vp, pt[None].contiguous(),
+                         torch.arange(40, dtype=torch.int32, device=dev),
+                         rows=torch.zeros(40, dtype=torch.int32, device=dev), inv_freq=freq)
+    fused = torch.zeros_like(s.fused[0], device=dev)
+    q, k, v = fused.split([8, 2, 2], dim=1)
+    idx = torch.zeros((3, 1), dtype=torch.int32, device=dev)
+    at = torch.full((3,), -1, dtype=torch.int32, device=dev)
+    lens = torch.full((3,), 40, dtype=torch.int32, device=dev)
+    out = torch.empty((3, 8, 128), dtype=torch.bfloat16, device=dev)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sha.append_decode_paged(q, k, v, kp, vp, idx, at, lens, table, inv_freq=freq, prefix_len=40,
+                                prefix_table=pt, scale=128 ** -0.5, out=out)
+    for t in range(9):
+        fused.copy_(s.fused[t])
+        idx.copy_(s.idx[t])
+        at.fill_(40 + t)
+        lens.fill_(41 + t)
+        out.fill_(9.0)
+        graph.replay()
+        assert torch.equal(out.cpu(), want[t])
+    assert sha.sha_get_device_status() == sha.SHA_OK
+
+
+def test_refusals(sha):
+    s = Steps(2, 4, 2, 64, 1, 16, 2, 8, torch.float16, seed=9)
+    q, k, v = (x.cuda() for x in s.split(0))
+    i = torch.zeros(2, dtype=torch.int32, device="cuda")
+    args = (s.k_pages.cuda(), s.v_pages.cuda(), s.idx[0].cuda(), i, i + 1, s.table.cuda())
+    with pytest.raises(ValueError):
+        sha.append_decode_paged(q[:1], k, v, *args)
+    with pytest.raises(ValueError):
+        sha.append_decode_paged(q[0], k, v, *args)
+    with pytest.raises(ValueError):                       # not contiguous, and nothing turns it
+        sha.append_decode_paged(s.fused[0].cuda()[:, :4], k, v, *args)
+
+
+def test_waits_that_give_up(sha):
+    """With the test build's wait limit at 1 ns the shared-prefix call's waits run out: it returns,
+    reports the timeout, and the next call with the limit restored is right.  In a process of its
+    own, since the test build is another library."""
+    from head_sparse_decode_b200 import build
+    script = textwrap.dedent("""
+        import ctypes, torch
+        import head_sparse_decode_b200 as sha
+        from prefix_reference import Case
+        sha._lib.sha_test_set_wait_limit.argtypes = [ctypes.c_ulonglong]
+        for c in (Case(40, 16, 2, 128, 2, 700, 300, 16, "bf16", seed=3),
+                  Case(5, 4, 4, 64, 2, 300, 40, 8, "fp16", seed=4),
+                  Case(3, 32, 2, 128, 1, 200, 100, 64, "fp16", seed=5)):
+            q, kp, vp, idx, lens, table, pt = c.on()
+            out = torch.zeros_like(q)
+            call = lambda: sha.sha_decode_prefix(q, kp, vp, idx, lens, table, c.prefix, pt, c.scale, out)
+            assert sha._lib.sha_test_set_wait_limit(1) == 0
+            call()
+            assert sha.sha_get_device_status() == sha.SHA_ERR_TIMEOUT
+            assert sha._lib.sha_test_set_wait_limit(4000000000) == 0
+            out.fill_(-77.0)
+            call()
+            assert sha.sha_get_device_status() == sha.SHA_OK
+            c.check(out, *c.reference(), -77.0)
+        print("waits gave up and recovered")
+    """)
+    env = dict(os.environ, SHA_DECODE_LIBRARY=build.build_test_hooks(),
+               PYTHONPATH=os.pathsep.join([ROOT, os.path.join(ROOT, "tests")]))
+    r = subprocess.run([sys.executable, "-c", script], env=env, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+    assert "waits gave up and recovered" in r.stdout
