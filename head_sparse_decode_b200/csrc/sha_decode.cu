@@ -434,6 +434,37 @@ sha_status_t kv_tensor_map(CUtensorMap *map, const void *base, sha_dtype_t dtype
     return SHA_OK;
 }
 
+// 5-D view [64 elements][8 keys][d/64][groups of 8 keys][pages and heads] of a page
+// pool, boxes of box_rows keys of one page (page_size and box_rows multiples of 8)
+// with 128-byte swizzle: the order KeyGroups wants in shared memory.
+sha_status_t kv_tensor_map_groups(CUtensorMap *map, const void *base, sha_dtype_t dtype, int d,
+                                  int page_size, long long planes, int box_rows)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (!encode) {
+        std::snprintf(g_last_cuda_error, sizeof g_last_cuda_error,
+                      "cuTensorMapEncodeTiled is not available from the driver");
+        return SHA_ERR_LAUNCH;
+    }
+    cuuint64_t dims[5] = {64, 8, (cuuint64_t)d / 64, (cuuint64_t)page_size / 8, (cuuint64_t)planes};
+    cuuint64_t strides[4] = {(cuuint64_t)d * 2, 128, (cuuint64_t)d * 16,
+                             (cuuint64_t)page_size * d * 2};
+    cuuint32_t box[5] = {64, 8, (cuuint32_t)d / 64, (cuuint32_t)box_rows / 8, 1};
+    cuuint32_t elem[5] = {1, 1, 1, 1, 1};
+    CUresult r = encode(map,
+                        dtype == SHA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                        5, const_cast<void *>(base), dims, strides, box, elem,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        std::snprintf(g_last_cuda_error, sizeof g_last_cuda_error,
+                      "cuTensorMapEncodeTiled failed with CUresult %d", (int)r);
+        return SHA_ERR_LAUNCH;
+    }
+    return SHA_OK;
+}
+
 // 4-D view [d, o1, o2, o3] of a strided K or V cache: d contiguous, the outer
 // dimensions (token, head, batch in the order of increasing stride) with the
 // given sizes and byte strides, boxes of box_d x box_rows tokens (1 along the
@@ -938,13 +969,13 @@ sha_status_t launch_prefix(const sha::PrefixParams &prm, const void *k, const vo
     const int suffix_box = prm.page_size < Suffix::kStage ? prm.page_size : Suffix::kStage;
     const long long planes = (long long)prm.num_pages * prm.H_kv;
     CUtensorMap tm_k, tm_v, ts_k, ts_v;
-    sha_status_t st = kv_tensor_map(&tm_k, k, dtype, D, prm.page_size, planes, box_rows);
-    if (st == SHA_OK) st = kv_tensor_map(&tm_v, v, dtype, D, prm.page_size, planes, box_rows);
+    sha_status_t st = kv_tensor_map_groups(&tm_k, k, dtype, D, prm.page_size, planes, box_rows);
+    if (st == SHA_OK) st = kv_tensor_map_groups(&tm_v, v, dtype, D, prm.page_size, planes, box_rows);
     ts_k = tm_k;
     ts_v = tm_v;
     if (suffix_box != box_rows) {
-        if (st == SHA_OK) st = kv_tensor_map(&ts_k, k, dtype, D, prm.page_size, planes, suffix_box);
-        if (st == SHA_OK) st = kv_tensor_map(&ts_v, v, dtype, D, prm.page_size, planes, suffix_box);
+        if (st == SHA_OK) st = kv_tensor_map_groups(&ts_k, k, dtype, D, prm.page_size, planes, suffix_box);
+        if (st == SHA_OK) st = kv_tensor_map_groups(&ts_v, v, dtype, D, prm.page_size, planes, suffix_box);
     }
     if (st != SHA_OK) return st;
     cudaError_t e = launch_kernel(prm.H_q / prm.H_kv > 8 ? tall : low, num_sms, C::kThreads,

@@ -28,7 +28,7 @@
 //
 // How a tile is computed.  Two streams of 128 query rows share the tensor cores, in
 // steps of 64 keys:
-//   * a producer warp brings the K and V tiles into a ring with TMA, in the order
+//   * one warp brings the K tiles, one the V tiles into a ring with TMA, in the order
 //     in which they are used;
 //   * one warp per stream issues its products: S = Q K^T (both operands in shared
 //     memory) into 64 columns of tensor memory, O += P V (P from 32 columns of
@@ -101,8 +101,9 @@ struct PrefixMergeParams {
 
 template <int D>
 struct PrefixConfig {
-    using Tile = GqaConfig<D>;                       // key tiles and their swizzle
-    static constexpr int kThreads = 384;             // producer, 2 MMA, 1 spare warp; 2 x 4 softmax warps
+    using Tile = GqaConfig<D>;                       // key tiles
+    static constexpr int kGroupBytes = KeyGroups<D>::kBytes;
+    static constexpr int kThreads = 384;             // K, 2 MMA, V; 2 x 4 softmax warps
     static constexpr int kSoftmax = 256;
     static constexpr int kSoftmaxWarp = 4;           // the first one
     static constexpr int kStreamRows = 128;
@@ -117,7 +118,8 @@ struct PrefixConfig {
     static constexpr int kBars = 2 * kBufs + 2 + 2 + 2 + 2 + 2 + 2;
     static constexpr int kCtlOffset = kBarOffset + 8 * kBars + 8;   // abort, mode, TMEM base
     static constexpr int kWarpOffset = kCtlOffset + 16;             // warp counts of the list
-    static constexpr int kUnitOffset = kWarpOffset + 4 * 8;         // a row tile's units
+    static constexpr int kLastOffset = kWarpOffset + 4 * 8;         // ring position last in each buffer
+    static constexpr int kUnitOffset = kLastOffset + 4 * kBufs;     // a row tile's units
     static constexpr int kQRowOffset = kUnitOffset + 4 * kRows;     // and the rows of q they are
     static constexpr int kStartOffset = kQRowOffset + 4 * kRows;    // first row tile of each head
     static constexpr int kPairOffset = kStartOffset + 4 * (kPrefixMaxHeads + 1);
@@ -390,7 +392,8 @@ struct PrefixSteps {
     __device__ __forceinline__ bool takes_last(int st) const { return pair || st < last_halves; }
 };
 
-// kNT: see suffix_worker.  tm_k, tm_v: boxes of up to 128 keys; ts_k, ts_v: of up to 32.
+// kNT: see suffix_worker.  Maps in groups of 8 keys (KeyGroups): tm_k, tm_v with boxes
+// of up to 128 keys, ts_k, ts_v of up to 32.
 template <typename T, int D, int kNT>
 __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
     sha_prefix_kernel(const PrefixParams p, const SuffixParams suffix,
@@ -421,6 +424,7 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
     volatile int *abort_flag = ctl, *paired = ctl + 1;
     int *warp_counts = reinterpret_cast<int *>(smem + C::kWarpOffset);
     int *unit_list = reinterpret_cast<int *>(smem + C::kUnitOffset);
+    volatile int *last_load = reinterpret_cast<volatile int *>(smem + C::kLastOffset);
     int *q_rows = reinterpret_cast<int *>(smem + C::kQRowOffset);
     int *start = reinterpret_cast<int *>(smem + C::kStartOffset);
     int *pairs = reinterpret_cast<int *>(smem + C::kPairOffset);
@@ -434,6 +438,7 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
         for (int s = 0; s < C::kBufs; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 2);                 // both streams have used the tile
+            last_load[s] = -1;
         }
         mbar_init(q_full, C::kSoftmax / 32);
         mbar_init(q_seen, 2);
@@ -501,66 +506,61 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
     auto wait_warp = [&](uint64_t *bar, uint32_t parity) {      // by a whole warp, agreed
         return (bool)__all_sync(0xffffffffu, wait(bar, parity));
     };
-    if (warp == 0) {
-        // -------------------------------------------------------- producer
+    if (warp == 0 || warp == 3) {
+        // -------------------------------------------------------- loads
         // every call reads the prefix again: the L2's default policy may keep it
         uint64_t policy;
         asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
-        uint32_t used = 0, last_parity = 0, pos = 0;
+        const bool is_k = warp == 0;
+        const CUtensorMap *map = is_k ? &tm_k : &tm_v;
+        uint32_t base = 0;
         const int box_rows = min(p.page_size, C::kTile);
-        // a tile's pages, one box per lane (at most 16), looked up a tile ahead of its K
-        auto rows_of = [&](int tile) { return min(C::kTile, p.keys - tile * C::kTile); };
-        auto pages_of = [&](int tile) {
-            return lane * box_rows < rows_of(tile)
-                       ? p.table[(tile * C::kTile + lane * box_rows) / p.page_size]
-                       : 0;
-        };
-        auto load = [&](int tile, int page, int h, const CUtensorMap *map) {
-            const int buf = (int)(pos % C::kBufs);
-            const uint32_t parity = (pos / C::kBufs) & 1u;
-            ++pos;
-            bool ok = true;
-            if (lane == 0) ok = wait(&empty[buf], parity ^ 1);
-            if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
-            const int rows = rows_of(tile);
-            const int chunks = (rows + box_rows - 1) / box_rows;
-            if (lane == 0)
-                mbar_arrive_expect_tx(&full[buf], (uint32_t)(chunks * Tile::kBoxes * box_rows * 128));
-            __syncwarp();
-            if (lane < chunks) {
-                if ((unsigned)page >= (unsigned)p.num_pages) {
-                    atomicOr(&g_sha_status, kStatusBadIndex);
-                    page = 0;                           // stay inside the pool
-                }
-                const int off = (tile * C::kTile + lane * box_rows) % p.page_size;
-                unsigned char *dst = smem + buf * C::kTileBytes + lane * box_rows * 128;
-#pragma unroll
-                for (int bx = 0; bx < Tile::kBoxes; ++bx)
-                    tma_load_3d(dst + bx * Tile::kBoxBytes, map, bx * 64, off, page * p.H_kv + h,
-                                &full[buf], policy);
-            }
-            last_parity = (last_parity & ~(1u << buf)) | (parity << buf);
-            used |= 1u << buf;
-            return true;
+        // a tile's pages, one per lane (at most 16), looked up a tile ahead
+        auto page_of = [&](int tile) {
+            const int key = tile * C::kTile + lane * box_rows;
+            return lane * box_rows < C::kTile && key < p.keys ? p.table[key / p.page_size] : 0;
         };
         bool ok = true;
         while (ok && wk.next(run)) {
-            // K_0, then K_i, V_(i-1), then the last V: the order of prefix_k_pos
-            int page = pages_of(run.first), next = 0;
-            if (run.n > 1) next = pages_of(run.first + 1);
-            ok = load(run.first, page, run.head, &tm_k);
-            for (int i = 1; ok && i < run.n; ++i) {
+            int next = page_of(run.first);
+            for (int i = 0; i < run.n; ++i) {
                 const int tile = run.first + i;
-                const int after = i + 1 < run.n ? pages_of(tile + 1) : 0;
-                ok = load(tile, next, run.head, &tm_k) && load(tile - 1, page, run.head, &tm_v);
-                page = next;
-                next = after;
+                int page = next;
+                if (i + 1 < run.n) next = page_of(tile + 1);
+                const uint32_t pos = base + (is_k ? prefix_k_pos(i) : prefix_v_pos(i, run.n));
+                const int buf = (int)(pos % C::kBufs);
+                const uint32_t parity = (pos / C::kBufs) & 1u;
+                if (lane == 0) ok = wait(&empty[buf], parity ^ 1);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                const int rows = min(C::kTile, p.keys - tile * C::kTile);
+                const int chunks = (rows + box_rows - 1) / box_rows;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&full[buf],
+                                          (uint32_t)(chunks * box_rows / 8 * C::kGroupBytes));
+                __syncwarp();
+                if (lane < chunks) {
+                    if ((unsigned)page >= (unsigned)p.num_pages) {
+                        atomicOr(&g_sha_status, kStatusBadIndex);
+                        page = 0;                       // stay inside the pool
+                    }
+                    const int off = (tile * C::kTile + lane * box_rows) % p.page_size;
+                    tma_load_groups(
+                        smem + buf * C::kTileBytes + lane * box_rows / 8 * C::kGroupBytes, map,
+                        off >> 3, page * p.H_kv + run.head, &full[buf], policy);
+                }
+                if (lane == 0) last_load[buf] = (int)pos;
             }
-            ok = ok && load(run.first + run.n - 1, page, run.head, &tm_v);
+            base += 2 * run.n;
         }
-        if (lane == 0)
+        // the copies still in flight after a wait that gave up: the last one of every
+        // buffer, whichever warp issued it (a buffer's phases alternate: one that has
+        // gone through two since cannot be told from one that has gone through none)
+        named_barrier(4, 64);
+        if (is_k && lane == 0)
             for (int s = 0; s < C::kBufs; ++s)
-                if (used & (1u << s)) mbar_wait_drain(&full[s], (last_parity >> s) & 1u);
+                if (last_load[s] >= 0)
+                    mbar_wait_drain(&full[s], ((uint32_t)last_load[s] / C::kBufs) & 1u);
         __syncwarp();
     } else if (warp <= 2) {
         // -------------------------------------------------------- products
@@ -571,9 +571,9 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
         // a descriptor's address field counts 16-byte units: tiles and k-steps add to
         // the whole
         const uint64_t q_desc = umma_desc_k_sw128(smem_addr(smem + C::kQOffset));
-        const uint64_t k_desc = umma_desc_k_sw128(smem_addr(smem));
-        const uint64_t v_desc = umma_desc_mn_sw128(smem_addr(smem), Tile::kBoxBytes, 1024);
-        constexpr uint32_t kHalf = C::kStep * 128 >> 4;            // 64 key rows of a box
+        const uint64_t k_desc = umma_desc_k_sw128(smem_addr(smem), C::kGroupBytes);
+        const uint64_t v_desc = umma_desc_mn_sw128(smem_addr(smem), 1024, C::kGroupBytes);
+        constexpr uint32_t kHalf = C::kStep / 8 * C::kGroupBytes >> 4;     // 64 keys
         const uint32_t s_at = tmem + st * C::kStep, o_at = tmem + C::kTmemO + st * D;
         const uint32_t p_at = tmem + C::kTmemP + st * (C::kStep / 2);
         bool ok = true;
@@ -597,9 +597,9 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
                                     (uint32_t)steps.half(st, step) * kHalf;
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
-                    constexpr int kBox = Tile::kBoxBytes >> 4;
-                    umma_f16_elected(leader, s_at, qd + (ks >> 2) * kBox + (ks & 3) * 2,
-                                     kd + (ks >> 2) * kBox + (ks & 3) * 2, kIdescS, ks > 0);
+                    umma_f16_elected(leader, s_at,
+                                     qd + (ks >> 2) * (Tile::kBoxBytes >> 4) + (ks & 3) * 2,
+                                     kd + (ks >> 2) * (1024 >> 4) + (ks & 3) * 2, kIdescS, ks > 0);
                 }
                 umma_commit_elected(leader, &s_full[st]);
                 if (steps.last_of_tile(st, step)) umma_commit_elected(leader, &empty[buf]);
@@ -626,7 +626,8 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
                                     (uint32_t)steps.half(st, step) * kHalf;
 #pragma unroll
                 for (int ks = 0; ks < C::kStep / 16; ++ks)
-                    umma_f16_tmem_a_elected(leader, o_at, p_at + ks * 8, vd + ks * (2048 >> 4),
+                    umma_f16_tmem_a_elected(leader, o_at, p_at + ks * 8,
+                                            vd + ks * (2 * C::kGroupBytes >> 4),
                                             kIdescO, ks > 0 ? 1u : step > 0);
                 umma_commit_elected(leader, &pv_done[st]);
                 if (steps.last_of_tile(st, step)) umma_commit_elected(leader, &empty[buf]);
@@ -779,13 +780,14 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
                     if (ok) ok = __all_sync(FULL, wait(&full[buf], (pos / C::kBufs) & 1u));
                     if (ok) {
                         unsigned char *vt = smem + buf * C::kTileBytes +
-                                            steps.half(st, step) * C::kStep * 128;
+                                            steps.half(st, step) * (C::kStep / 8) * C::kGroupBytes;
                         const int left = (C::kStep - rows) * Tile::kBoxes * 8;
                         for (int e = pair ? stid : stid & 127; e < left; e += pair ? 256 : 128) {
                             const int chunk = e & 7, bx = (e >> 3) % Tile::kBoxes;
                             const int key = rows + (e >> 3) / Tile::kBoxes;
-                            *reinterpret_cast<uint4 *>(vt + bx * Tile::kBoxBytes + key * 128 +
-                                                       chunk * 16) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4 *>(vt + (key >> 3) * C::kGroupBytes +
+                                                       bx * 1024 + (key & 7) * 128 + chunk * 16) =
+                                make_uint4(0, 0, 0, 0);
                         }
                         fence_proxy_async_shared();
                     }

@@ -50,21 +50,41 @@ struct SuffixParams {
     int slot_floats;
 };
 
+// How keys lie in shared memory here and in the prefix's tiles: groups of 8 keys, each
+// 64 elements of the 8 (128-byte rows, 1 KiB, 128-byte-swizzled), then the next 64.
+// One copy of a 5-D map [64 elements][8 keys][d/64][groups][pages and heads] brings
+// a whole run of keys of a page that way.  (Two boxes of [keys][64 elements] per run
+// take twice the copies, and a lone warp issues one in about 115 clocks: pages of 16
+// keys then bound the prefix at 3700 clocks a tile.)
+template <int D>
+struct KeyGroups {
+    static constexpr int kBytes = 1024 * (D / 64);
+};
+__device__ __forceinline__ void tma_load_groups(void *dst, const CUtensorMap *map, int group,
+                                                int plane, uint64_t *bar, uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%2, %2, %2, %3, %4}], [%5], %6;" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(group), "r"(plane), "r"(smem_addr(bar)),
+        "l"(policy)
+        : "memory");
+}
+
 template <int D>
 struct SuffixConfig {
     static constexpr int kWorkers = D == 128 ? 6 : 10;   // warps of the block at work
     static constexpr int kStage = 32;                    // keys
     static constexpr int kStages = 2;
     static constexpr int kBoxes = D / 64;
-    static constexpr int kBoxBytes = kStage * 128;
-    static constexpr int kTileBytes = kBoxes * kBoxBytes;        // K or V of a stage
+    static constexpr int kGroupBytes = KeyGroups<D>::kBytes;
+    static constexpr int kTileBytes = kStage / 8 * kGroupBytes;  // K or V of a stage
     static constexpr int kRingBytes = kStages * 2 * kTileBytes;
     // a unit's latency in stages: with 6 workers an SM streams a 32-key stage in
     // 0.37 us, and a unit costs a worker about 4 us, 0.7 us of the SM
     static constexpr int kUnitCost = 2;
     static constexpr int kMinWeight = 4;                 // of a worker's range
     static constexpr int kMaxRuns = 64;                  // of a unit, about
-    static_assert(4 * kBoxes * 2 <= 32, "one lane per box of 8 keys");
 };
 
 // Stages of a row's own keys (at least one: a row that ends with the prefix still
@@ -270,11 +290,11 @@ __device__ __forceinline__ void suffix_worker(const SuffixParams &p, const CUten
     const uint64_t policy = l2_policy_evict_first();
     const int box_shift = min(p.page_shift, 5);
     static_assert(C::kStage == 32, "boxes of up to 2^5 keys");
-    const int box_kv = lane & 1, box_d = (lane >> 1) % C::kBoxes, box_c = (lane >> 1) / C::kBoxes;
+    const int box_kv = lane & 1, box_c = lane >> 1;
     const CUtensorMap *box_map = box_kv ? &tm_v : &tm_k;
     const uint32_t box_bytes = (uint32_t)(2 * C::kBoxes * 128) << box_shift;   // a chunk, K and V
     unsigned char *box_dst =
-        ring + box_kv * C::kTileBytes + box_d * C::kBoxBytes + ((box_c * 128) << box_shift);
+        ring + box_kv * C::kTileBytes + (box_c << box_shift) / 8 * C::kGroupBytes;
     SuffixWalk lw = walk;
     SuffixRun lr, ln;                    // the run being loaded, the next one
     int lh, lnh = 0, li = 0;             // their head ids; the next stage of lr
@@ -309,8 +329,9 @@ __device__ __forceinline__ void suffix_worker(const SuffixParams &p, const CUten
                 atomicOr(&g_sha_status, kStatusBadIndex);
                 page = 0;                               // stay inside the pool
             }
-            tma_load_3d(box_dst + stage * 2 * C::kTileBytes, box_map, box_d * 64,
-                        key & ((1 << p.page_shift) - 1), page * p.H_kv + lh, &full[stage], policy);
+            tma_load_groups(box_dst + stage * 2 * C::kTileBytes, box_map,
+                            (key & ((1 << p.page_shift) - 1)) >> 3, page * p.H_kv + lh,
+                            &full[stage], policy);
         }
         ++issued;
         if (++li == lr.n) next_run();
@@ -324,8 +345,9 @@ __device__ __forceinline__ void suffix_worker(const SuffixParams &p, const CUten
     // ---- the products
     const int g = lane >> 2, qd = lane & 3, mi = lane >> 3, mr = lane & 7;
     // ldmatrix rows of this lane: K tiles are (keys, d), V^T tiles (d, keys)
-    const uint32_t k_row = smem_addr(ring) + ((mi & 1) * 8 + mr) * 128;
-    const uint32_t v_row = smem_addr(ring) + C::kTileBytes + ((mi >> 1) * 8 + mr) * 128;
+    const uint32_t k_row = smem_addr(ring) + (mi & 1) * C::kGroupBytes + mr * 128;
+    const uint32_t v_row =
+        smem_addr(ring) + C::kTileBytes + (mi >> 1) * C::kGroupBytes + mr * 128;
     const uint32_t k_half = (uint32_t)(mi >> 1), v_half = (uint32_t)(mi & 1);
     // the 16-byte chunk of a box row, swizzled by the row (which is mr modulo 8)
     auto chunk_at = [&](uint32_t chunk) { return ((chunk & 7) ^ (uint32_t)mr) << 4; };
@@ -395,7 +417,8 @@ __device__ __forceinline__ void suffix_worker(const SuffixParams &p, const CUten
                 for (int e = lane; e < C::kStage * C::kBoxes * 8; e += 32) {
                     const int chunk = e & 7, bx = (e >> 3) % C::kBoxes, kk = (e >> 3) / C::kBoxes;
                     if (kk >= rows || kk < lo)
-                        *reinterpret_cast<uint4 *>(v + bx * C::kBoxBytes + kk * 128 + chunk * 16) =
+                        *reinterpret_cast<uint4 *>(v + (kk >> 3) * C::kGroupBytes + bx * 1024 +
+                                                   (kk & 7) * 128 + chunk * 16) =
                             make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_shared();   // before the stage is refilled by TMA
@@ -415,7 +438,7 @@ __device__ __forceinline__ void suffix_worker(const SuffixParams &p, const CUten
 #pragma unroll
                 for (int kk = 0; kk < kKT; ++kk) {
                     uint32_t ka[4];
-                    ldmatrix_x4(kt + (ks >> 2) * C::kBoxBytes + kk * 16 * 128 +
+                    ldmatrix_x4(kt + (ks >> 2) * 1024 + kk * 2 * C::kGroupBytes +
                                     chunk_at(ks * 2 + k_half),
                                 ka);
 #pragma unroll
@@ -473,7 +496,7 @@ __device__ __forceinline__ void suffix_worker(const SuffixParams &p, const CUten
 #pragma unroll
                 for (int n = 0; n < D / 16; ++n) {
                     uint32_t va[4];
-                    ldmatrix_x4_trans(vt + (n >> 2) * C::kBoxBytes + kk * 16 * 128 +
+                    ldmatrix_x4_trans(vt + (n >> 2) * 1024 + kk * 2 * C::kGroupBytes +
                                           chunk_at(n * 2 + v_half),
                                       va);
 #pragma unroll

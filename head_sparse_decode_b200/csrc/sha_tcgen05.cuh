@@ -73,6 +73,18 @@ __device__ __forceinline__ uint64_t umma_desc_k_sw128(uint32_t addr)
     return d;
 }
 
+// The same with 8-row groups `sbo` bytes apart.
+__device__ __forceinline__ uint64_t umma_desc_k_sw128(uint32_t addr, uint32_t sbo)
+{
+    uint64_t d = 0;
+    d |= (uint64_t)((addr >> 4) & 0x3FFFu);
+    d |= (uint64_t)1u << 16;
+    d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)2u << 61;
+    return d;
+}
+
 // The same for a 64-byte swizzle: 64-byte rows (32 elements), 8-row groups
 // 512 bytes apart, layout type 4.
 __device__ __forceinline__ uint64_t umma_desc_k_sw64(uint32_t addr)

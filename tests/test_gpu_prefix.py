@@ -280,3 +280,34 @@ def test_python_refusals_on_the_gpu(sha):
     assert e.value.status == sha.SHA_ERR_UNSUPPORTED
     call(q=q[:, :, None])
     assert sha.sha_get_device_status() == sha.SHA_OK
+
+
+def test_many_calls_back_to_back(sha):
+    """Calls that follow one another without a pause, each beginning while the last one ends: none
+    waits for anything that has gone by (a bounded wait would cost it seconds)."""
+    cases = [Case(32, 64, 8, 128, 5, 384, 60, 16, "bf16", seed=101),
+             Case(24, 12, 12, 128, 4, 640, 33, 8, "fp16", seed=102),
+             Case(16, 8, 8, 64, 4, 900, 70, 32, "bf16", seed=103)]
+    args = [c.on() for c in cases]
+    outs = [torch.full_like(a[0], FILL) for a in args]
+
+    def calls():
+        for _ in range(4):
+            for c, a, o in zip(cases, args, outs):
+                sha.sha_decode_prefix(*a[:6], c.prefix, a[6], c.scale, o)
+
+    calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    begin.record()
+    for _ in range(10):
+        graph.replay()
+    end.record()
+    torch.cuda.synchronize()
+    assert begin.elapsed_time(end) < 1000.0
+    assert sha.sha_get_device_status() == sha.SHA_OK
+    for c, o in zip(cases, outs):
+        c.check(o, *c.reference(), FILL)
