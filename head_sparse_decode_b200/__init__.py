@@ -287,6 +287,7 @@ def sha_decode_prefix(q, k_pages, v_pages, batch_head_index, seqlens, block_tabl
     rows cover the whole sequences, their entries for the prefix unread.  workspace
     (default: a new tensor) is uint8, at least sha_decode_prefix_workspace_size bytes;
     calls that share it must not overlap."""
+    prefix_len = int(prefix_len)
     pool, q_shape, dtype, index = k_pages.shape, q.shape, k_pages.dtype, k_pages.get_device()
     code, i32 = _DTYPE_CODES.get(dtype), torch.int32
     idx_shape, table_shape = batch_head_index.shape, block_table.shape

@@ -1157,6 +1157,7 @@ sha_status_t sha_decode_prefix(const void *q, const void *k_pages, const void *v
     DeviceInfo *info;
     st = current_device(&dev, &info);
     if (st != SHA_OK) return st;
+    if (info->num_sms < 2) return SHA_ERR_UNSUPPORTED;   // the two parts run side by side
     const PrefixPlan pl = make_prefix_plan(B, H_q, H_kv, d, top_k, info->num_sms);
     if (!workspace || workspace_bytes < pl.bytes) return SHA_ERR_WORKSPACE;
     char *ws = static_cast<char *>(workspace);

@@ -45,7 +45,7 @@
 // So a step's exponentials run beside the next step's S and the last one's P V.
 // (Steps of 128 keys leave P no columns of its own but S's: each product then waits
 // for the one before it and the exponentials for both, 4840 clocks for a tile of 256
-// rows by 128 keys against %%.)
+// rows by 128 keys against 4350.)
 // A row tile of more than 128 rows gives each stream 128 of them and every key of a
 // tile (bound by the exponentials, 16 a clock, and the products, about level); one
 // of up to 128 rows gives both streams the same rows and one half of each key tile
@@ -323,9 +323,10 @@ struct PrefixCut {
 // the slower of the two parts is done first, out of 32 evenly spaced ones, one per
 // lane of the calling warp.  Times in ns, measured: a run's beginning and end; a key
 // tile of 128 keys by up to 128 rows, and by more; a worker's beginning; an SM's
-// share of a weight of the suffix (32 keys' bytes, per 64 elements of d).
-constexpr float kPrefixRunNs = 8000.f, kPrefixTileNs = 1500.f, kPrefixWideNs = 2450.f;
-constexpr float kSuffixRunNs = 5000.f, kSuffixWeightNs = 80.f;
+// share of a weight of the suffix (32 keys' bytes, per 64 elements of d).  The choice is
+// flat around them: 20 % more or less on any moved no case by more than 1 %.
+constexpr float kPrefixRunNs = 10000.f, kPrefixTileNs = 1600.f, kPrefixWideNs = 2450.f;
+constexpr float kSuffixRunNs = 5000.f, kSuffixWeightNs = 100.f;
 __device__ __forceinline__ int prefix_share(int row_tiles, int wide, int tiles, long long weights,
                                             int d64, int blocks)
 {
@@ -841,7 +842,7 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
                 }
                 // the streams of a pair take turns at the exponentials: each then has the
                 // unit, which they saturate, to itself while the other one reads its next
-                // scores (1500 clocks a step against 2360 in step with each other)
+                // scores (2175 clocks a step against 2360 in step with each other)
                 if (pair) named_barrier(2 + st, C::kSoftmax);
                 if (ok && busy) {
                     const float m0 = m_ref == -INFINITY ? 0.f : m_ref;
