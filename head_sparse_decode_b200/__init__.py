@@ -319,9 +319,7 @@ def sha_decode_prefix(q, k_pages, v_pages, batch_head_index, seqlens, block_tabl
     handle = _raw_stream(stream, dev)
     if workspace is None:
         nbytes = _prefix_workspace_size(B, H_q, H_kv, d, top_k, index)
-        workspace = seqlens.new_empty((nbytes + 3) // 4)
-        if stream is not None:
-            _record_on(workspace, stream, dev)
+        workspace = _made_for(stream, dev, lambda: seqlens.new_empty((nbytes + 3) // 4))
     else:
         if workspace.get_device() != index or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {dev}")
@@ -642,12 +640,18 @@ def _raw_stream(stream, device):
     return _stream_handle(stream, device)
 
 
-def _record_on(t, stream, device):
-    """Keep t's memory until `stream` is done with it, where that is not the stream t was
-    allocated on."""
+def _made_for(stream, device, make):
+    """make() with `stream` current, so that a tensor it allocates belongs to the stream that
+    will use it: memory that the current stream's pending work still uses is not given to it."""
+    if stream is None:
+        return make()
     handle = _stream_handle(stream, device)
-    if handle != torch._C._cuda_getCurrentRawStream(device.index):
-        t.record_stream(torch.cuda.ExternalStream(handle, device=device))
+    if handle == torch._C._cuda_getCurrentRawStream(device.index):
+        return make()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(handle, device=device)
+    with torch.cuda.stream(stream):
+        return make()
 
 
 def _on_device(device, entry, args):
@@ -764,8 +768,8 @@ def rope_frequencies(rotary, base=10000.0, scaling=None, device=None):
 def sha_rope(x, positions, inv_freq, out=None, interleaved=False, mscale=1.0, stream=None):
     """Rotary positions: x [T, H, d] (any strides, d contiguous; float16 or bfloat16),
     positions int32 [T], inv_freq float64 [rotary/2] (rope_frequencies), all on one
-    device.  out (default: a new contiguous tensor) may be x itself.  Rotating by
-    -positions is the inverse up to mscale^2, and the gradient."""
+    device.  out (default: a new contiguous tensor, which belongs to `stream`) may be x
+    itself.  Rotating by -positions is the inverse up to mscale^2, and the gradient."""
     shape, index, dtype = x.shape, x.get_device(), x.dtype
     xs = x.stride()
     code = _DTYPE_CODES.get(dtype)
@@ -781,7 +785,8 @@ def sha_rope(x, positions, inv_freq, out=None, interleaved=False, mscale=1.0, st
         code = _dtype_code(dtype)
     T, H, d = shape
     if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        out = _made_for(stream, x.device,
+                        lambda: torch.empty_like(x, memory_format=torch.contiguous_format))
     os_ = out.stride()
     device = x.device
     _on_device(device, _lib.sha_rope,
@@ -846,7 +851,8 @@ def sha_append_paged(k, v, k_pages, v_pages, block_table, positions, rows=None, 
             if q_shape[0] != T or q_shape[2] != d:
                 raise ValueError("q must be [T, H_q, d]")
         if q_out is None:
-            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            q_out = _made_for(stream, q.device,
+                              lambda: torch.empty_like(q, memory_format=torch.contiguous_format))
         else:
             _check_heads_view("q_out", q_out, dtype, index)
             if q_out.shape != q_shape:
@@ -905,13 +911,12 @@ def append_decode_paged(q, k, v, k_pages, v_pages, batch_head_index, positions, 
         sha_append_paged(k, v, k_pages, v_pages, block_table, positions, stream=stream)
         turned = q
     else:
-        turned = torch.empty_like(q, memory_format=torch.contiguous_format)
-        if stream is not None and q.is_cuda:
-            _record_on(turned, stream, q.device)
-        sha_append_paged(k, v, k_pages, v_pages, block_table, positions, inv_freq=inv_freq,
-                         interleaved=interleaved, mscale=mscale, q=q, q_out=turned, stream=stream)
+        turned = sha_append_paged(k, v, k_pages, v_pages, block_table, positions,
+                                  inv_freq=inv_freq, interleaved=interleaved, mscale=mscale, q=q,
+                                  stream=stream)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _made_for(stream, q.device,
+                        lambda: torch.empty_like(q, memory_format=torch.contiguous_format))
     if prefix_len > 0:
         return sha_decode_prefix(turned, k_pages, v_pages, batch_head_index, seqlens, block_table,
                                  prefix_len, prefix_table, scale, out, workspace=workspace,

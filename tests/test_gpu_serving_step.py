@@ -135,6 +135,27 @@ def test_decode_steps_on_another_stream(sha):
     assert all(torch.equal(a, b) for a, b in zip(first, other))
 
 
+def test_new_tensors_belong_to_the_stream_that_uses_them(sha):
+    """Memory just freed on the current stream, whose work on it may be pending, is not handed to
+    a call on another stream."""
+    other = torch.cuda.Stream()
+    x = torch.zeros((512, 16, 128), dtype=torch.float16, device="cuda")
+    pos = torch.zeros(512, dtype=torch.int32, device="cuda")
+    freq = torch.zeros(64, dtype=torch.float64, device="cuda")
+    torch.cuda.synchronize()
+    for stream in (other, other.cuda_stream):
+        freed = torch.empty_like(x)
+        at = freed.data_ptr()
+        del freed
+        out = sha.sha_rope(x, pos, freq, stream=stream)
+        assert out.data_ptr() != at
+        other.synchronize()
+        del out
+        again = torch.empty_like(x)                       # it is still the current stream's
+        assert again.data_ptr() == at
+        del again
+
+
 def test_captured_step(sha):
     """A step captured once and replayed for each token: positions and lengths move on the device."""
     s = Steps(3, 8, 2, 128, 1, 40, 9, 8, torch.bfloat16, seed=8)
