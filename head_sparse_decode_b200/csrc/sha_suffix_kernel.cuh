@@ -296,7 +296,7 @@ __device__ __forceinline__ void suffix_worker(const SuffixParams &p, const CUten
     unsigned char *box_dst =
         ring + box_kv * C::kTileBytes + (box_c << box_shift) / 8 * C::kGroupBytes;
     SuffixWalk lw = walk;
-    SuffixRun lr, ln;                    // the run being loaded, the next one
+    SuffixRun lr = {}, ln = {};          // the run being loaded, the next one
     int lh, lnh = 0, li = 0;             // their head ids; the next stage of lr
     bool more, next_more;
     int page = 0, chunks = 0, key = 0;   // that stage: this lane's page, boxes, this lane's key
