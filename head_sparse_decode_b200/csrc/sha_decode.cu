@@ -1400,6 +1400,29 @@ sha_status_t sha_test_set_wait_limit(unsigned long long ns)
     if (e != cudaSuccess) return launch_error(e);
     return SHA_OK;
 }
+
+// The steps that stream `st` takes through a run of `tiles` key tiles, the last with
+// `rows` keys: three numbers a step (tile, half, whether it is the stream's last one of
+// the tile), then whether the stream has a step in the last tile; returns the count.
+int sha_test_prefix_steps(int pair, int tiles, int rows, int st, int *out)
+{
+    const sha::PrefixSteps steps(pair != 0, tiles, rows);
+    const int n = steps.count(st);
+    for (int i = 0; i < n; ++i) {
+        out[3 * i] = steps.tile(i);
+        out[3 * i + 1] = steps.half(st, i);
+        out[3 * i + 2] = steps.last_of_tile(st, i);
+    }
+    out[3 * n] = steps.takes_last(st);
+    return n;
+}
+
+// Ring positions of tile i's K and V in a run of n.
+void sha_test_prefix_ring(int i, int n, int out[2])
+{
+    out[0] = sha::prefix_k_pos(i);
+    out[1] = sha::prefix_v_pos(i, n);
+}
 #endif
 
 sha_status_t sha_copy_bandwidth_probe(void *dst, const void *src, size_t bytes, void *stream)

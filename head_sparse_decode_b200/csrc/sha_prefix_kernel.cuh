@@ -364,8 +364,8 @@ __device__ __forceinline__ int prefix_share(int row_tiles, int wide, int tiles, 
 
 // Ring position of a run's K and V tiles: K_0, then K_i, V_(i-1) for i = 1 .. n-1,
 // then V_(n-1) -- the order in which the products use them.
-__device__ __forceinline__ int prefix_k_pos(int i) { return i == 0 ? 0 : 2 * i - 1; }
-__device__ __forceinline__ int prefix_v_pos(int i, int n) { return i < n - 1 ? 2 * i + 2 : 2 * n - 1; }
+__host__ __device__ __forceinline__ int prefix_k_pos(int i) { return i == 0 ? 0 : 2 * i - 1; }
+__host__ __device__ __forceinline__ int prefix_v_pos(int i, int n) { return i < n - 1 ? 2 * i + 2 : 2 * n - 1; }
 
 // The steps of 64 keys that the two streams take through a run of `tiles` key
 // tiles, the last with `rows` keys: paired streams take both halves of every tile,
@@ -374,23 +374,23 @@ struct PrefixSteps {
     bool pair;
     int tiles, last_halves;          // halves of the last tile that hold keys: 1 or 2
 
-    __device__ __forceinline__ PrefixSteps(bool pair_, int tiles_, int rows)
+    __host__ __device__ __forceinline__ PrefixSteps(bool pair_, int tiles_, int rows)
         : pair(pair_), tiles(tiles_), last_halves(rows > 64 ? 2 : 1)
     {
     }
-    __device__ __forceinline__ int count(int st) const
+    __host__ __device__ __forceinline__ int count(int st) const
     {
         return pair ? 2 * tiles - 2 + last_halves : st < last_halves ? tiles : tiles - 1;
     }
-    __device__ __forceinline__ int tile(int step) const { return pair ? step >> 1 : step; }
-    __device__ __forceinline__ int half(int st, int step) const { return pair ? step & 1 : st; }
+    __host__ __device__ __forceinline__ int tile(int step) const { return pair ? step >> 1 : step; }
+    __host__ __device__ __forceinline__ int half(int st, int step) const { return pair ? step & 1 : st; }
     // whether no later step of the stream needs this step's tile
-    __device__ __forceinline__ bool last_of_tile(int st, int step) const
+    __host__ __device__ __forceinline__ bool last_of_tile(int st, int step) const
     {
         return !pair || (step & 1) || step == count(st) - 1;
     }
     // whether the stream has a step in the last tile
-    __device__ __forceinline__ bool takes_last(int st) const { return pair || st < last_halves; }
+    __host__ __device__ __forceinline__ bool takes_last(int st) const { return pair || st < last_halves; }
 };
 
 // kNT: see suffix_worker.  Maps in groups of 8 keys (KeyGroups): tm_k, tm_v with boxes
@@ -633,9 +633,18 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
                 umma_commit_elected(leader, &pv_done[st]);
                 if (steps.last_of_tile(st, step)) umma_commit_elected(leader, &empty[buf]);
             }
-            if (ok && !steps.takes_last(st) && lane == 0) {       // a tile without this stream
-                mbar_arrive(&empty[(base + prefix_k_pos(n - 1)) % C::kBufs]);
-                mbar_arrive(&empty[(base + prefix_v_pos(n - 1, n)) % C::kBufs]);
+            // A tile without this stream: it gives up K and V of it, too, but only once they
+            // have arrived, and behind its own products.  (Given up before, this would count
+            // for the tile that the buffer still holds, in place of the other stream's; given
+            // up by a plain arrival, it could overtake this stream's last P V, and a load two
+            // rounds of the ring ahead would take that one's buffer for free.)
+            if (!steps.takes_last(st)) {
+                const uint32_t k_at = base + prefix_k_pos(n - 1);
+                const uint32_t v_at = base + prefix_v_pos(n - 1, n);
+                ok = ok && wait_warp(&full[k_at % C::kBufs], (k_at / C::kBufs) & 1u);
+                if (ok) umma_commit_elected(leader, &empty[k_at % C::kBufs]);
+                ok = ok && wait_warp(&full[v_at % C::kBufs], (v_at / C::kBufs) & 1u);
+                if (ok) umma_commit_elected(leader, &empty[v_at % C::kBufs]);
             }
             base += 2 * n;
         }

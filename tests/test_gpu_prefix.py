@@ -79,6 +79,18 @@ def test_long_prefix_split_over_many_blocks(sha, prefix):
     _check(sha, Case(3, 2, 2, 64, 1, prefix, 0, 128, "fp16", seed=prefix + 1))
 
 
+@pytest.mark.parametrize("B,H_q,H_kv,d,top_k,prefix,page_size,dtype", [
+    (8, 72, 72, 128, 18, 1930, 16, "fp16"), (8, 80, 80, 64, 20, 1345, 64, "bf16"),
+    (6, 160, 40, 128, 20, 1984, 32, "bf16"), (5, 90, 90, 64, 36, 2049, 8, "fp16")])
+def test_long_runs_that_end_in_a_short_tile(sha, B, H_q, H_kv, d, top_k, prefix, page_size, dtype):
+    """Many heads of few rows each: runs of many key tiles, the last with up to 64 keys, in which
+    the second stream has no step."""
+    c = Case(B, H_q, H_kv, d, top_k, prefix, 9, page_size, dtype, seed=prefix)
+    first = _check(sha, c)
+    for _ in range(5):
+        assert torch.equal(_run(sha, c), first)
+
+
 def test_suffixes_longer_than_the_prefix(sha):
     """Own keys split over blocks and joined with the shared part."""
     _check(sha, Case(2, 8, 1, 128, 1, 9, 3000, 16, "bf16", seed=12))
