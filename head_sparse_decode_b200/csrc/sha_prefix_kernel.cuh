@@ -825,6 +825,7 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
                 if (step > 0) {
                     if (ok) ok = __all_sync(FULL, wait(&pv_done[st], pv_parity));
                     pv_parity ^= 1;
+                    tc_fence_after_sync();        // P and O are written next
                 }
                 if (ok && busy) {
                     // the first step sets the reference, later ones move it rarely
@@ -832,7 +833,6 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
                     if (__any_sync(FULL, move)) {
                         const float m_new = move ? top : m_ref;
                         if (step > 0) {
-                            tc_fence_after_sync();
                             const float a = move ? exp2_approx(m_ref - m_new) : 1.f;
                             l0 *= a;
                             l1 *= a;
