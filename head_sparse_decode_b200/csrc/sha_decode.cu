@@ -1417,6 +1417,50 @@ int sha_test_prefix_steps(int pair, int tiles, int rows, int st, int *out)
     return n;
 }
 
+// How the row tiles of a prefix are cut: start[h], pairs[h] of the heads as
+// prefix_row_tiles leaves them, `tiles` key tiles a row tile, `share` blocks.  Five
+// numbers a run (block, row tile, head, first tile, tiles) and, for a row tile's first
+// run, the blocks that share it (else 0); returns the runs, and the blocks in use.
+int sha_test_prefix_cut(const int *start, const int *pairs, int heads, int tiles, int share,
+                        int blocks, int *used, int *out)
+{
+    int n = 0;
+    *used = 0;
+    for (int c = 0; c < blocks; ++c) {
+        sha::PrefixCut cut;
+        sha::PrefixRun run;
+        cut.plan(start, pairs, heads, (unsigned)tiles, (unsigned)share, (unsigned)c);
+        *used = (int)cut.used;
+        if (c >= *used) break;
+        while (cut.next(run)) {
+            int *o = out + 6 * n++;
+            o[0] = c;
+            o[1] = run.row_tile;
+            o[2] = run.head;
+            o[3] = run.first;
+            o[4] = run.n;
+            o[5] = run.first == 0 ? cut.sharers(run, (unsigned)c) : 0;
+        }
+    }
+    return n;
+}
+
+// The blocks that a call gives the prefix, as prefix_share chooses them.
+int sha_test_prefix_share(int row_tiles, int wide, int tiles, long long weights, int d64, int blocks)
+{
+    int best = 0;
+    float least = INFINITY;
+    for (int i = 0; i < 32; ++i) {
+        const int share = sha::prefix_share_at(i, blocks);
+        const float t = sha::prefix_share_ns(share, row_tiles, wide, tiles, weights, d64, blocks);
+        if (t < least || (t == least && share < best)) {
+            least = t;
+            best = share;
+        }
+    }
+    return best;
+}
+
 // Ring positions of tile i's K and V in a run of n.
 void sha_test_prefix_ring(int i, int n, int out[2])
 {

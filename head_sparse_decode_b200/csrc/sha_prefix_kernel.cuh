@@ -221,19 +221,19 @@ struct PrefixCut {
     unsigned t, t_end;           // this block's range
     int own_pieces;              // (pieces) those of this block's row tile
 
-    __device__ __forceinline__ unsigned begin(unsigned c) const
+    __host__ __device__ __forceinline__ unsigned begin(unsigned c) const
     {
         return c * base + min(c, extra);
     }
     // First block of head h, under pieces.
-    __device__ __forceinline__ unsigned block_of(int h) const
+    __host__ __device__ __forceinline__ unsigned block_of(int h) const
     {
         return (unsigned)start[h] * pieces + (unsigned)pairs[h] * (pieces2 - pieces);
     }
     // The last head whose first f(head) is at most x: among equal ones the last is
     // the one that has row tiles.
     template <class F>
-    __device__ __forceinline__ int search(unsigned x, F f) const
+    __host__ __device__ __forceinline__ int search(unsigned x, F f) const
     {
         int lo = 0, hi = heads;
         while (hi - lo > 1) {
@@ -243,7 +243,7 @@ struct PrefixCut {
         }
         return lo;
     }
-    __device__ __forceinline__ void plan(const int *start_, const int *pairs_, int heads_,
+    __host__ __device__ __forceinline__ void plan(const int *start_, const int *pairs_, int heads_,
                                          unsigned tiles, unsigned grid, unsigned block)
     {
         start = start_;
@@ -280,15 +280,15 @@ struct PrefixCut {
             return;
         }
         const unsigned blocks = min(total, grid);
-        used = blocks;
         const unsigned even = (total + blocks - 1) / blocks + 2 * kRunTiles;
         const unsigned whole = (row_tiles + blocks - 1) / blocks;
         if (whole * (tiles + kRunTiles) <= even) {
+            used = (row_tiles + whole - 1) / whole;
             t = min(block * whole, row_tiles) * tiles;
             t_end = min((block + 1) * whole, row_tiles) * tiles;
-            base = whole * tiles;                    // begin() of a block in use
             return;
         }
+        used = blocks;
         base = total / blocks;
         extra = total - base * blocks;
         if (block < blocks) {
@@ -296,7 +296,7 @@ struct PrefixCut {
             t_end = begin(block + 1);
         }
     }
-    __device__ __forceinline__ bool next(PrefixRun &r)
+    __host__ __device__ __forceinline__ bool next(PrefixRun &r)
     {
         if (t >= t_end) return false;
         r.row_tile = (int)div_fast(t, key_tiles);
@@ -308,7 +308,7 @@ struct PrefixCut {
         return true;
     }
     // Blocks that share the row tile which this block's run begins.
-    __device__ __forceinline__ int sharers(const PrefixRun &r, unsigned block) const
+    __host__ __device__ __forceinline__ int sharers(const PrefixRun &r, unsigned block) const
     {
         if (r.first + r.n == (int)key_tiles) return 1;
         if (pieces) return own_pieces;
@@ -327,29 +327,47 @@ struct PrefixCut {
 // flat around them: 20 % more or less on any moved no case by more than 1 %.
 constexpr float kPrefixRunNs = 10000.f, kPrefixTileNs = 1600.f, kPrefixWideNs = 2450.f;
 constexpr float kSuffixRunNs = 5000.f, kSuffixWeightNs = 100.f;
-__device__ __forceinline__ int prefix_share(int row_tiles, int wide, int tiles, long long weights,
-                                            int d64, int blocks)
+
+// A quotient for the estimates below, the division approximate on the device.
+__host__ __device__ __forceinline__ float div_approx(float a, float b)
 {
-    const int lane = threadIdx.x & 31;
-    const int share = max(1, min(blocks - 1, (lane + 1) * blocks / 33));
+#ifdef __CUDA_ARCH__
+    return __fdividef(a, b);
+#else
+    return a / b;
+#endif
+}
+// The i-th share tried, and the time that the call takes with it.
+__host__ __device__ __forceinline__ int prefix_share_at(int i, int blocks)
+{
+    return max(1, min(blocks - 1, (i + 1) * blocks / 33));
+}
+__host__ __device__ __forceinline__ float prefix_share_ns(int share, int row_tiles, int wide,
+                                                          int tiles, long long weights, int d64,
+                                                          int blocks)
+{
     const int weight = row_tiles + wide;
     float t;
-    // (an estimate: in floats, the divisions approximate)
     const float f = (float)tiles;
     if (weight <= share) {
-        const float per = __fdividef((float)share + 0.5f, (float)weight);
+        const float per = div_approx((float)share + 0.5f, (float)weight);
         const float p1 = fminf(floorf(per), f), p2 = fminf(floorf(2.f * per), f);
-        t = fmaxf(row_tiles > wide ? ceilf(__fdividef(f, p1) - 1e-3f) * kPrefixTileNs : 0.f,
-                  wide > 0 ? ceilf(__fdividef(f, p2) - 1e-3f) * kPrefixWideNs : 0.f) +
+        t = fmaxf(row_tiles > wide ? ceilf(div_approx(f, p1) - 1e-3f) * kPrefixTileNs : 0.f,
+                  wide > 0 ? ceilf(div_approx(f, p2) - 1e-3f) * kPrefixWideNs : 0.f) +
             kPrefixRunNs;
     } else {
-        const float each = __fdividef(1.f, (float)share);
+        const float each = div_approx(1.f, (float)share);
         t = ((float)(row_tiles - wide) * kPrefixTileNs + (float)wide * kPrefixWideNs) * f * each +
             ceilf((float)row_tiles * each) * kPrefixRunNs;
     }
-    t = fmaxf(t, kSuffixRunNs +
-                     __fdividef((float)weights * (kSuffixWeightNs * (float)d64), (float)(blocks - share)));
-    int best = share;
+    return fmaxf(t, kSuffixRunNs + div_approx((float)weights * (kSuffixWeightNs * (float)d64),
+                                              (float)(blocks - share)));
+}
+__device__ __forceinline__ int prefix_share(int row_tiles, int wide, int tiles, long long weights,
+                                            int d64, int blocks)
+{
+    int best = prefix_share_at(threadIdx.x & 31, blocks);
+    float t = prefix_share_ns(best, row_tiles, wide, tiles, weights, d64, blocks);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
         const float x = __shfl_xor_sync(0xffffffffu, t, off);

@@ -100,9 +100,11 @@ __device__ __forceinline__ int suffix_stages(const SuffixParams &p, int len, int
 // in a lone warp, 150 clocks each in 32 bits and 700 in 64.  For a < 2^20 a float
 // quotient is exact: (a + 1/2) / b lies at least 1/(2b) from an integer, and the
 // approximate division (2 ulp) is off by at most 2^-22 of a quotient below 2^20 / b.
-__device__ __forceinline__ unsigned div_fast(unsigned a, unsigned b)
+__host__ __device__ __forceinline__ unsigned div_fast(unsigned a, unsigned b)
 {
+#ifdef __CUDA_ARCH__
     if (a < (1u << 20)) return (unsigned)__fdividef((float)a + 0.5f, (float)min(b, 1u << 24));
+#endif
     return a / b;
 }
 __device__ __forceinline__ long long div_fast(long long a, long long b)
