@@ -70,3 +70,17 @@ class Plan:
                 assert blocks_of[row_tile] == list(range(block, block + sharers))
         # every block that counts as in use has work; the others take the rows' own keys
         assert self.used == len({run[0] for run in self.runs})
+
+
+# Calls whose blocks take several row tiles each (their own keys, too many for the prefix to
+# get a block for each row tile): arguments of prefix_reference.Case
+SEVERAL_ROW_TILES = [
+    (3, 300, 300, 64, 200, 300, 400, 32, "fp16"),        # narrow row tiles, some split
+    (2, 260, 260, 128, 260, 330, 600, 16, "fp16"),
+    (2, 160, 160, 128, 160, 1025, 300, 32, "fp16"),      # nine key tiles, the last of one key
+    (2, 160, 160, 64, 160, 1070, 150, 8, "bf16"),
+    (1, 1000, 1000, 128, 1000, 40, 60, 8, "fp16"),       # one key tile: whole row tiles
+    (40, 800, 100, 64, 100, 300, 130, 16, "bf16"),       # wide row tiles between narrow ones
+    (40, 800, 100, 128, 40, 340, 130, 32, "bf16"),
+    (36, 400, 100, 64, 100, 100, 90, 8, "fp16"),
+]

@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+from prefix_plan import SEVERAL_ROW_TILES
 from prefix_reference import Case
 
 pytestmark = pytest.mark.gpu
@@ -87,6 +88,17 @@ def test_long_runs_that_end_in_a_short_tile(sha, B, H_q, H_kv, d, top_k, prefix,
     the second stream has no step."""
     c = Case(B, H_q, H_kv, d, top_k, prefix, 9, page_size, dtype, seed=prefix)
     first = _check(sha, c)
+    for _ in range(5):
+        assert torch.equal(_run(sha, c), first)
+
+
+@pytest.mark.parametrize("args", SEVERAL_ROW_TILES, ids=str)
+def test_blocks_of_several_row_tiles(sha, args):
+    """One block takes row tile after row tile: other queries, other heads, wide and narrow ones,
+    pieces of split ones."""
+    c = Case(*args, seed=args[5])
+    first = _run(sha, c)
+    _check(sha, c, rows=sorted({c.B - 1, c.B // 4} if c.B > 3 else {c.B - 1}))
     for _ in range(5):
         assert torch.equal(_run(sha, c), first)
 

@@ -3,7 +3,8 @@ import random
 
 import pytest
 
-from prefix_plan import Plan
+from prefix_plan import SEVERAL_ROW_TILES, Plan
+from prefix_reference import Case
 
 
 @pytest.fixture(scope="module")
@@ -37,3 +38,17 @@ def test_whole_row_tiles_count_only_the_blocks_that_have_some(library):
     p = Plan(library, [200] * 7, 1, 128, 128, share=5)
     p.check()
     assert p.used == 4
+
+
+@pytest.mark.parametrize("args", SEVERAL_ROW_TILES, ids=str)
+def test_calls_whose_blocks_take_several_row_tiles(library, args):
+    """The calls that the GPU tests make for these blocks do reach them."""
+    p = Plan.of(library, Case(*args, seed=args[5]))
+    p.check()
+    per = p.runs_of_block()
+    assert max(per) >= 2 and sum(n >= 2 for n in per) >= p.used // 2
+    if p.wide and p.wide < p.row_tiles:          # a paired row tile and another in one block
+        kinds = {}
+        for block, row_tile, head, _, _, _ in p.runs:
+            kinds.setdefault(block, set()).add(row_tile + 1 < p.start[head + 1])
+        assert args[4] < args[2] or any(len(k) == 2 for k in kinds.values())
