@@ -893,6 +893,11 @@ def _explain_append(k, v, k_pages, v_pages, block_table, positions, rows, inv_fr
         _check_contiguous("inv_freq", inv_freq, 1, torch.float64, index)
 
 
+_lib.sha_append_decode_paged.argtypes = [_vp] * 13 + [_i, _i, _f, _vp, _vp] + [_i] * 9 + [
+    _f, _vp, _i, _vp, ctypes.c_size_t, _vp]
+_lib.sha_append_decode_paged.restype = _i
+
+
 def append_decode_paged(q, k, v, k_pages, v_pages, batch_head_index, positions, seqlens,
                         block_table, inv_freq=None, interleaved=False, mscale=1.0, prefix_len=0,
                         prefix_table=None, scale=None, out=None, workspace=None, stream=None):
@@ -904,25 +909,100 @@ def append_decode_paged(q, k, v, k_pages, v_pages, batch_head_index, positions, 
 
     q [B, H_q, d] and k, v [B, H_kv, d] are views with d contiguous (slices of a fused
     projection's rows); out [B, H_q, d] is new if not given, its unselected rows then
-    uninitialised.  Without inv_freq q must be contiguous."""
+    uninitialised.  Without inv_freq q must be contiguous.  A call that is refused has
+    written nothing."""
     if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
         raise ValueError("q must be [B, H_q, d] and k [B, H_kv, d]")
-    if inv_freq is None:
-        sha_append_paged(k, v, k_pages, v_pages, block_table, positions, stream=stream)
-        turned = q
-    else:
-        turned = sha_append_paged(k, v, k_pages, v_pages, block_table, positions,
-                                  inv_freq=inv_freq, interleaved=interleaved, mscale=mscale, q=q,
-                                  stream=stream)
+    prefix_len = int(prefix_len)
+    (B, H_q, d), shape, pool, index, dtype = q.shape, k.shape, k_pages.shape, k.get_device(), k.dtype
+    qs, ks, vs = q.stride(), k.stride(), v.stride()
+    code, i32 = _DTYPE_CODES.get(dtype), torch.int32
+    # one pass over what has to hold; a call that fails it is explained step by step
+    if not (index >= 0 and code is not None and v.shape == shape
+            and qs[2] == 1 and ks[2] == 1 and vs[2] == 1
+            and q.dtype is dtype and v.dtype is dtype
+            and q.get_device() == index and v.get_device() == index
+            and len(pool) == 4 and pool[1] == shape[1] and pool[3] == d and v_pages.shape == pool
+            and k_pages.dtype is dtype and v_pages.dtype is dtype
+            and k_pages.get_device() == index and v_pages.get_device() == index
+            and k_pages.is_contiguous() and v_pages.is_contiguous()
+            and all(t.dtype is i32 and t.get_device() == index and t.is_contiguous()
+                    for t in (batch_head_index, positions, seqlens, block_table))
+            and batch_head_index.dim() == 2 and batch_head_index.shape[0] == B
+            and block_table.dim() == 2 and block_table.shape[0] == B
+            and positions.shape == (B,) and seqlens.shape == (B,)
+            and (q.is_contiguous() if inv_freq is None else
+                 inv_freq.dtype is torch.float64 and inv_freq.dim() == 1
+                 and inv_freq.get_device() == index and inv_freq.is_contiguous())
+            and (prefix_len == 0
+                 or (prefix_len > 0 and prefix_table is not None and prefix_table.dim() == 1
+                     and prefix_table.shape[0] * pool[2] >= prefix_len
+                     and prefix_table.dtype is i32 and prefix_table.get_device() == index
+                     and prefix_table.is_contiguous()))
+            and (out is None or (out.numel() == B * H_q * d and out.dtype is dtype
+                                 and out.get_device() == index and out.is_contiguous()))
+            and (workspace is None or (workspace.get_device() == index
+                                       and workspace.is_contiguous()))):
+        _explain_step(q, k, v, k_pages, v_pages, batch_head_index, positions, seqlens, block_table,
+                      inv_freq, prefix_len, prefix_table, out, workspace)
+        code = _dtype_code(dtype)
+    H_kv, top_k, max_pages = shape[1], batch_head_index.shape[1], block_table.shape[1]
+    device = k.device
+    handle = _raw_stream(stream, device)
+    turned, nbytes = None, 0
+    if inv_freq is not None:
+        turned = _made_for(stream, device,
+                           lambda: torch.empty_like(q, memory_format=torch.contiguous_format))
     if out is None:
-        out = _made_for(stream, q.device,
+        out = _made_for(stream, device,
                         lambda: torch.empty_like(q, memory_format=torch.contiguous_format))
+    if prefix_len > 0 and workspace is None:
+        nbytes = _prefix_workspace_size(B, H_q, H_kv, d, top_k, index)
+        workspace = _made_for(stream, device, lambda: seqlens.new_empty((nbytes + 3) // 4))
+    elif workspace is not None:
+        nbytes = workspace.numel() * workspace.element_size()
+    _on_device(device, _lib.sha_append_decode_paged,
+               (q.data_ptr(), _stride_pair(qs[0], qs[1]), k.data_ptr(), _stride_pair(ks[0], ks[1]),
+                v.data_ptr(), _stride_pair(vs[0], vs[1]), k_pages.data_ptr(), v_pages.data_ptr(),
+                block_table.data_ptr(), batch_head_index.data_ptr(), positions.data_ptr(),
+                seqlens.data_ptr(), None if inv_freq is None else inv_freq.data_ptr(),
+                0 if inv_freq is None else 2 * inv_freq.shape[0], 1 if interleaved else 0, mscale,
+                None if turned is None else turned.data_ptr(),
+                None if prefix_len == 0 else prefix_table.data_ptr(), prefix_len, B, H_q, H_kv,
+                pool[0], pool[2], max_pages, d, top_k, _default_scale(scale, d), out.data_ptr(),
+                code, None if workspace is None else workspace.data_ptr(), nbytes, handle))
+    return out
+
+
+def _explain_step(q, k, v, k_pages, v_pages, batch_head_index, positions, seqlens, block_table,
+                  inv_freq, prefix_len, prefix_table, out, workspace):
+    _explain_append(k, v, k_pages, v_pages, block_table, positions, None, inv_freq)
+    index, dtype = k.get_device(), k.dtype
+    _check_heads_view("q", q, dtype, index)
+    B, H_q, d = q.shape
+    if inv_freq is None and not q.is_contiguous():
+        raise ValueError("q must be contiguous: without inv_freq nothing turns it")
+    if block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, max_pages]")
+    _check_contiguous("batch_head_index", batch_head_index, 2, torch.int32, index)
+    if batch_head_index.shape[0] != B:
+        raise ValueError("batch_head_index must be [B, top_k]")
+    _check_vector("seqlens", seqlens, B, index)
+    if prefix_len < 0:
+        raise ValueError("prefix_len must not be negative")
     if prefix_len > 0:
-        return sha_decode_prefix(turned, k_pages, v_pages, batch_head_index, seqlens, block_table,
-                                 prefix_len, prefix_table, scale, out, workspace=workspace,
-                                 stream=stream)
-    return sha_decode_paged(turned, k_pages, v_pages, batch_head_index, seqlens, block_table, scale,
-                            out, stream=stream)
+        if prefix_table is None:
+            raise ValueError("prefix_len needs prefix_table")
+        _check_contiguous("prefix_table", prefix_table, 1, torch.int32, index)
+        if prefix_table.shape[0] * k_pages.shape[2] < prefix_len:
+            raise ValueError("prefix_table must hold ceil(prefix_len / page_size) page ids")
+    if out is not None:
+        _check_contiguous("out", out, out.dim(), dtype, index)
+        if out.numel() != B * H_q * d:
+            raise ValueError("out must hold [B, H_q, d] elements")
+    if workspace is not None and (workspace.get_device() != index
+                                  or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
 
 
 def sha_get_device_status(stream=None, device=None):

@@ -772,7 +772,7 @@ sha_status_t decode_impl(const void *q, const void *k, const void *v, const int3
                          void *out, sha_dtype_t dtype, void *workspace,
                          size_t workspace_bytes, int num_splits, void *stream,
                          bool library_workspace, const KvLayout &lay = KvLayout(),
-                         ForcedCluster force = ForcedCluster())
+                         ForcedCluster force = ForcedCluster(), bool launch = true)
 {
     const int32_t *seqlens = lay.seqlens;
     if (dtype != SHA_FP16 && dtype != SHA_BF16) return SHA_ERR_UNSUPPORTED;
@@ -837,6 +837,7 @@ sha_status_t decode_impl(const void *q, const void *k, const void *v, const int3
         workspace_bytes = owned[dev].bytes;
     }
     if (need > 0 && (!workspace || workspace_bytes < need)) return SHA_ERR_WORKSPACE;
+    if (!launch) return SHA_OK;
 
     sha::DecodeParams prm;
     prm.q = q;
@@ -992,76 +993,12 @@ sha_status_t launch_prefix(const sha::PrefixParams &prm, const void *k, const vo
     return SHA_OK;
 }
 
-__global__ void copy_probe_kernel(uint4 *__restrict__ dst, const uint4 *__restrict__ src,
-                                  size_t n)
-{
-    const size_t stride = (size_t)gridDim.x * blockDim.x;
-    size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x;
-    for (; i + 3 * stride < n; i += 4 * stride) {
-        const uint4 a = __ldcs(src + i);
-        const uint4 b = __ldcs(src + i + stride);
-        const uint4 c = __ldcs(src + i + 2 * stride);
-        const uint4 d = __ldcs(src + i + 3 * stride);
-        __stcs(dst + i, a);
-        __stcs(dst + i + stride, b);
-        __stcs(dst + i + 2 * stride, c);
-        __stcs(dst + i + 3 * stride, d);
-    }
-    for (; i < n; i += stride) __stcs(dst + i, __ldcs(src + i));
-}
-
-}  // namespace
-
-// The other translation units of the library: their launch errors, read by
-// sha_last_cuda_error(), and their sticky device flags, taken and cleared.
-sha_status_t sha_launch_failed(cudaError_t e) { return launch_error(e); }
-unsigned sha_rope_take_status();   // sha_rope.cu
-
-extern "C" {
-
-sha_status_t sha_decode(const void *q, const void *k, const void *v,
-                        const int32_t *batch_head_index, int B, int H_q, int H_kv, int N_kv,
-                        int d, int top_k, float scale, void *out, void *stream)
-{
-    return decode_impl(q, k, v, batch_head_index, B, H_q, H_kv, N_kv, d, top_k, scale, out,
-                       SHA_FP16, nullptr, 0, 0, stream, true);
-}
-
-sha_status_t sha_decode_bf16(const void *q, const void *k, const void *v,
-                             const int32_t *batch_head_index, int B, int H_q, int H_kv,
-                             int N_kv, int d, int top_k, float scale, void *out, void *stream)
-{
-    return decode_impl(q, k, v, batch_head_index, B, H_q, H_kv, N_kv, d, top_k, scale, out,
-                       SHA_BF16, nullptr, 0, 0, stream, true);
-}
-
-sha_status_t sha_decode_ex(const void *q, const void *k, const void *v,
-                           const int32_t *batch_head_index, int B, int H_q, int H_kv,
-                           int N_kv, int d, int top_k, float scale, void *out,
-                           sha_dtype_t dtype, void *workspace, size_t workspace_bytes,
-                           int num_splits, void *stream)
-{
-    return decode_impl(q, k, v, batch_head_index, B, H_q, H_kv, N_kv, d, top_k, scale, out,
-                       dtype, workspace, workspace_bytes, num_splits, stream, false);
-}
-
-sha_status_t sha_decode_varlen(const void *q, const void *k, const void *v,
-                               const int32_t *batch_head_index, const int32_t *seqlens, int B,
-                               int H_q, int H_kv, int N_max, int d, int top_k, float scale,
-                               void *out, sha_dtype_t dtype, void *stream)
-{
-    if (B > 0 && top_k > 0 && !seqlens) return SHA_ERR_INVALID_ARG;
-    KvLayout lay;
-    lay.seqlens = seqlens;
-    return decode_impl(q, k, v, batch_head_index, B, H_q, H_kv, N_max, d, top_k, scale, out,
-                       dtype, nullptr, 0, 0, stream, true, lay);
-}
-
-sha_status_t sha_decode_paged(const void *q, const void *k_pages, const void *v_pages,
-                              const int32_t *batch_head_index, const int32_t *seqlens,
-                              const int32_t *block_table, int B, int H_q, int H_kv,
-                              int num_pages, int page_size, int max_pages, int d, int top_k,
-                              float scale, void *out, sha_dtype_t dtype, void *stream)
+// sha_decode_paged and sha_decode_prefix, or (launch false) their checks alone.
+sha_status_t paged_call(const void *q, const void *k_pages, const void *v_pages,
+                        const int32_t *batch_head_index, const int32_t *seqlens,
+                        const int32_t *block_table, int B, int H_q, int H_kv,
+                        int num_pages, int page_size, int max_pages, int d, int top_k,
+                        float scale, void *out, sha_dtype_t dtype, void *stream, bool launch)
 {
     if (num_pages < 1 || page_size < 1 || max_pages < 1) return SHA_ERR_INVALID_ARG;
     if ((long long)max_pages * page_size > (1 << 30)) return SHA_ERR_INVALID_ARG;
@@ -1076,61 +1013,16 @@ sha_status_t sha_decode_paged(const void *q, const void *k_pages, const void *v_
     lay.num_pages = num_pages;
     return decode_impl(q, k_pages, v_pages, batch_head_index, B, H_q, H_kv,
                        max_pages * page_size, d, top_k, scale, out, dtype, nullptr, 0, 0,
-                       stream, true, lay);
+                       stream, true, lay, ForcedCluster(), launch);
 }
 
-sha_status_t sha_decode_strided(const void *q, const void *k, const void *v,
-                                const int32_t *batch_head_index, const int32_t *seqlens, int B,
-                                int H_q, int H_kv, int N_kv, int d, int top_k, float scale,
-                                void *out, const int64_t k_strides[3], const int64_t v_strides[3],
-                                sha_dtype_t dtype, void *stream)
-{
-    if (!k_strides || !v_strides) return SHA_ERR_INVALID_ARG;
-    KvLayout lay;
-    lay.strided = true;
-    lay.seqlens = seqlens;
-    lay.k_strides = {k_strides[0], k_strides[1], k_strides[2]};
-    lay.v_strides = {v_strides[0], v_strides[1], v_strides[2]};
-    for (int i = 0; i < 3; ++i) {
-        if (k_strides[i] < 1 || v_strides[i] < 1) return SHA_ERR_INVALID_ARG;
-        // TMA: every stride a multiple of 16 bytes, below 2^40 bytes
-        if (k_strides[i] % 8 || v_strides[i] % 8) return SHA_ERR_MISALIGNED;
-        if (k_strides[i] >= (1ll << 39) || v_strides[i] >= (1ll << 39)) return SHA_ERR_INVALID_ARG;
-    }
-    return decode_impl(q, k, v, batch_head_index, B, H_q, H_kv, N_kv, d, top_k, scale, out,
-                       dtype, nullptr, 0, 0, stream, true, lay);
-}
-
-sha_status_t sha_decode_tokens(const void *q, const void *k, const void *v,
-                               const int32_t *batch_head_index, const int32_t *tokens, int B,
-                               int H_q, int H_kv, int N_kv, int d, int top_k, int n_sel,
-                               float scale, void *out, sha_dtype_t dtype, void *stream)
-{
-    if (n_sel < 1) return SHA_ERR_INVALID_ARG;
-    if (B > 0 && top_k > 0 && !tokens) return SHA_ERR_INVALID_ARG;
-    KvLayout lay;
-    lay.tokens = tokens;
-    lay.n_sel = n_sel;
-    return decode_impl(q, k, v, batch_head_index, B, H_q, H_kv, N_kv, d, top_k, scale, out,
-                       dtype, nullptr, 0, 0, stream, true, lay);
-}
-
-size_t sha_decode_prefix_workspace_size(int B, int H_q, int H_kv, int d, int top_k)
-{
-    if (check_prefix_shape(B, H_q, H_kv, d, top_k) != SHA_OK || B == 0 || top_k == 0) return 0;
-    int dev;
-    DeviceInfo *info;
-    if (current_device(&dev, &info) != SHA_OK) return 0;
-    return make_prefix_plan(B, H_q, H_kv, d, top_k, info->num_sms).bytes;
-}
-
-sha_status_t sha_decode_prefix(const void *q, const void *k_pages, const void *v_pages,
-                               const int32_t *batch_head_index, const int32_t *seqlens,
-                               const int32_t *block_table, const int32_t *prefix_table,
-                               int prefix_len, int B, int H_q, int H_kv, int num_pages,
-                               int page_size, int max_pages, int d, int top_k, float scale,
-                               void *out, sha_dtype_t dtype, void *workspace,
-                               size_t workspace_bytes, void *stream)
+sha_status_t prefix_call(const void *q, const void *k_pages, const void *v_pages,
+                         const int32_t *batch_head_index, const int32_t *seqlens,
+                         const int32_t *block_table, const int32_t *prefix_table,
+                         int prefix_len, int B, int H_q, int H_kv, int num_pages,
+                         int page_size, int max_pages, int d, int top_k, float scale,
+                         void *out, sha_dtype_t dtype, void *workspace,
+                         size_t workspace_bytes, void *stream, bool launch)
 {
     if (dtype != SHA_FP16 && dtype != SHA_BF16) return SHA_ERR_UNSUPPORTED;
     if (num_pages < 1 || page_size < 1 || max_pages < 1 || prefix_len < 1) return SHA_ERR_INVALID_ARG;
@@ -1160,6 +1052,7 @@ sha_status_t sha_decode_prefix(const void *q, const void *k_pages, const void *v
     if (info->num_sms < 2) return SHA_ERR_UNSUPPORTED;   // the two parts run side by side
     const PrefixPlan pl = make_prefix_plan(B, H_q, H_kv, d, top_k, info->num_sms);
     if (!workspace || workspace_bytes < pl.bytes) return SHA_ERR_WORKSPACE;
+    if (!launch) return SHA_OK;
     char *ws = static_cast<char *>(workspace);
 
     sha::PrefixParams prm;
@@ -1228,6 +1121,179 @@ sha_status_t sha_decode_prefix(const void *q, const void *k_pages, const void *v
                                                         dev, s)
                     : launch_prefix<__nv_bfloat16, 64>(prm, k_pages, v_pages, suf, mrg, dtype, sms,
                                                        dev, s);
+}
+
+__global__ void copy_probe_kernel(uint4 *__restrict__ dst, const uint4 *__restrict__ src,
+                                  size_t n)
+{
+    const size_t stride = (size_t)gridDim.x * blockDim.x;
+    size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x;
+    for (; i + 3 * stride < n; i += 4 * stride) {
+        const uint4 a = __ldcs(src + i);
+        const uint4 b = __ldcs(src + i + stride);
+        const uint4 c = __ldcs(src + i + 2 * stride);
+        const uint4 d = __ldcs(src + i + 3 * stride);
+        __stcs(dst + i, a);
+        __stcs(dst + i + stride, b);
+        __stcs(dst + i + 2 * stride, c);
+        __stcs(dst + i + 3 * stride, d);
+    }
+    for (; i < n; i += stride) __stcs(dst + i, __ldcs(src + i));
+}
+
+}  // namespace
+
+// The other translation units of the library: their launch errors, read by
+// sha_last_cuda_error(), and their sticky device flags, taken and cleared.
+sha_status_t sha_launch_failed(cudaError_t e) { return launch_error(e); }
+unsigned sha_rope_take_status();   // sha_rope.cu
+sha_status_t sha_append_call(      // sha_rope.cu: sha_append_paged, or its checks alone
+    const void *k, const void *v, const int64_t k_strides[2], const int64_t v_strides[2], int T,
+    int H_kv, int d, void *k_pages, void *v_pages, const int32_t *block_table,
+    const int32_t *rows, const int32_t *positions, int B, int num_pages, int page_size,
+    int max_pages, const double *inv_freq, int rotary, int interleaved, float mscale,
+    const void *q, const int64_t q_strides[2], int H_q, void *q_out, const int64_t q_out_strides[2],
+    sha_dtype_t dtype, void *stream, bool launch);
+
+extern "C" {
+
+sha_status_t sha_decode(const void *q, const void *k, const void *v,
+                        const int32_t *batch_head_index, int B, int H_q, int H_kv, int N_kv,
+                        int d, int top_k, float scale, void *out, void *stream)
+{
+    return decode_impl(q, k, v, batch_head_index, B, H_q, H_kv, N_kv, d, top_k, scale, out,
+                       SHA_FP16, nullptr, 0, 0, stream, true);
+}
+
+sha_status_t sha_decode_bf16(const void *q, const void *k, const void *v,
+                             const int32_t *batch_head_index, int B, int H_q, int H_kv,
+                             int N_kv, int d, int top_k, float scale, void *out, void *stream)
+{
+    return decode_impl(q, k, v, batch_head_index, B, H_q, H_kv, N_kv, d, top_k, scale, out,
+                       SHA_BF16, nullptr, 0, 0, stream, true);
+}
+
+sha_status_t sha_decode_ex(const void *q, const void *k, const void *v,
+                           const int32_t *batch_head_index, int B, int H_q, int H_kv,
+                           int N_kv, int d, int top_k, float scale, void *out,
+                           sha_dtype_t dtype, void *workspace, size_t workspace_bytes,
+                           int num_splits, void *stream)
+{
+    return decode_impl(q, k, v, batch_head_index, B, H_q, H_kv, N_kv, d, top_k, scale, out,
+                       dtype, workspace, workspace_bytes, num_splits, stream, false);
+}
+
+sha_status_t sha_decode_varlen(const void *q, const void *k, const void *v,
+                               const int32_t *batch_head_index, const int32_t *seqlens, int B,
+                               int H_q, int H_kv, int N_max, int d, int top_k, float scale,
+                               void *out, sha_dtype_t dtype, void *stream)
+{
+    if (B > 0 && top_k > 0 && !seqlens) return SHA_ERR_INVALID_ARG;
+    KvLayout lay;
+    lay.seqlens = seqlens;
+    return decode_impl(q, k, v, batch_head_index, B, H_q, H_kv, N_max, d, top_k, scale, out,
+                       dtype, nullptr, 0, 0, stream, true, lay);
+}
+
+sha_status_t sha_decode_paged(const void *q, const void *k_pages, const void *v_pages,
+                              const int32_t *batch_head_index, const int32_t *seqlens,
+                              const int32_t *block_table, int B, int H_q, int H_kv,
+                              int num_pages, int page_size, int max_pages, int d, int top_k,
+                              float scale, void *out, sha_dtype_t dtype, void *stream)
+{
+    return paged_call(q, k_pages, v_pages, batch_head_index, seqlens, block_table, B, H_q, H_kv,
+                      num_pages, page_size, max_pages, d, top_k, scale, out, dtype, stream, true);
+}
+
+sha_status_t sha_decode_strided(const void *q, const void *k, const void *v,
+                                const int32_t *batch_head_index, const int32_t *seqlens, int B,
+                                int H_q, int H_kv, int N_kv, int d, int top_k, float scale,
+                                void *out, const int64_t k_strides[3], const int64_t v_strides[3],
+                                sha_dtype_t dtype, void *stream)
+{
+    if (!k_strides || !v_strides) return SHA_ERR_INVALID_ARG;
+    KvLayout lay;
+    lay.strided = true;
+    lay.seqlens = seqlens;
+    lay.k_strides = {k_strides[0], k_strides[1], k_strides[2]};
+    lay.v_strides = {v_strides[0], v_strides[1], v_strides[2]};
+    for (int i = 0; i < 3; ++i) {
+        if (k_strides[i] < 1 || v_strides[i] < 1) return SHA_ERR_INVALID_ARG;
+        // TMA: every stride a multiple of 16 bytes, below 2^40 bytes
+        if (k_strides[i] % 8 || v_strides[i] % 8) return SHA_ERR_MISALIGNED;
+        if (k_strides[i] >= (1ll << 39) || v_strides[i] >= (1ll << 39)) return SHA_ERR_INVALID_ARG;
+    }
+    return decode_impl(q, k, v, batch_head_index, B, H_q, H_kv, N_kv, d, top_k, scale, out,
+                       dtype, nullptr, 0, 0, stream, true, lay);
+}
+
+sha_status_t sha_decode_tokens(const void *q, const void *k, const void *v,
+                               const int32_t *batch_head_index, const int32_t *tokens, int B,
+                               int H_q, int H_kv, int N_kv, int d, int top_k, int n_sel,
+                               float scale, void *out, sha_dtype_t dtype, void *stream)
+{
+    if (n_sel < 1) return SHA_ERR_INVALID_ARG;
+    if (B > 0 && top_k > 0 && !tokens) return SHA_ERR_INVALID_ARG;
+    KvLayout lay;
+    lay.tokens = tokens;
+    lay.n_sel = n_sel;
+    return decode_impl(q, k, v, batch_head_index, B, H_q, H_kv, N_kv, d, top_k, scale, out,
+                       dtype, nullptr, 0, 0, stream, true, lay);
+}
+
+size_t sha_decode_prefix_workspace_size(int B, int H_q, int H_kv, int d, int top_k)
+{
+    if (check_prefix_shape(B, H_q, H_kv, d, top_k) != SHA_OK || B == 0 || top_k == 0) return 0;
+    int dev;
+    DeviceInfo *info;
+    if (current_device(&dev, &info) != SHA_OK) return 0;
+    return make_prefix_plan(B, H_q, H_kv, d, top_k, info->num_sms).bytes;
+}
+
+sha_status_t sha_decode_prefix(const void *q, const void *k_pages, const void *v_pages,
+                               const int32_t *batch_head_index, const int32_t *seqlens,
+                               const int32_t *block_table, const int32_t *prefix_table,
+                               int prefix_len, int B, int H_q, int H_kv, int num_pages,
+                               int page_size, int max_pages, int d, int top_k, float scale,
+                               void *out, sha_dtype_t dtype, void *workspace,
+                               size_t workspace_bytes, void *stream)
+{
+    return prefix_call(q, k_pages, v_pages, batch_head_index, seqlens, block_table, prefix_table,
+                       prefix_len, B, H_q, H_kv, num_pages, page_size, max_pages, d, top_k, scale,
+                       out, dtype, workspace, workspace_bytes, stream, true);
+}
+
+sha_status_t sha_append_decode_paged(
+    const void *q, const int64_t q_strides[2], const void *k, const int64_t k_strides[2],
+    const void *v, const int64_t v_strides[2], void *k_pages, void *v_pages,
+    const int32_t *block_table, const int32_t *batch_head_index, const int32_t *positions,
+    const int32_t *seqlens, const double *inv_freq, int rotary, int interleaved, float mscale,
+    void *q_turned, const int32_t *prefix_table, int prefix_len, int B, int H_q, int H_kv,
+    int num_pages, int page_size, int max_pages, int d, int top_k, float scale, void *out,
+    sha_dtype_t dtype, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (prefix_len < 0 || H_q < 1) return SHA_ERR_INVALID_ARG;
+    const int64_t rows[2] = {(int64_t)H_q * d, d};
+    const bool turn = rotary > 0;
+    const void *queries = turn ? q_turned : q;
+    // both calls' checks, then both calls
+    for (const bool launch : {false, true}) {
+        sha_status_t st = sha_append_call(
+            k, v, k_strides, v_strides, B, H_kv, d, k_pages, v_pages, block_table, nullptr,
+            positions, B, num_pages, page_size, max_pages, inv_freq, rotary, interleaved, mscale,
+            turn ? q : nullptr, q_strides, turn ? H_q : 0, q_turned, rows, dtype, stream, launch);
+        if (st == SHA_OK)
+            st = prefix_len > 0
+                     ? prefix_call(queries, k_pages, v_pages, batch_head_index, seqlens,
+                                   block_table, prefix_table, prefix_len, B, H_q, H_kv, num_pages,
+                                   page_size, max_pages, d, top_k, scale, out, dtype, workspace,
+                                   workspace_bytes, stream, launch)
+                     : paged_call(queries, k_pages, v_pages, batch_head_index, seqlens,
+                                  block_table, B, H_q, H_kv, num_pages, page_size, max_pages, d,
+                                  top_k, scale, out, dtype, stream, launch);
+        if (st != SHA_OK) return st;
+    }
+    return SHA_OK;
 }
 
 size_t sha_decode_workspace_size(int B, int H_q, int H_kv, int N_kv, int d, int top_k,

@@ -495,6 +495,30 @@ sha_status_t sha_append_paged(const void *k, const void *v, const int64_t k_stri
                               void *stream);
 
 /*
+ * sha_append_decode_paged -- one decode step of a layer: sha_append_paged for one
+ * token of each of B rows (row b's at positions[b]), then sha_decode_prefix for
+ * prefix_len >= 1 or sha_decode_paged for prefix_len = 0, on one stream.  Both
+ * calls' arguments are checked before the first is enqueued: a refused step has
+ * written nothing.
+ *   q, k, v     : [B, H_q, d] and [B, H_kv, d] views as in sha_append_paged; with
+ *                 rotary = 0 q is contiguous and read as it is (q_strides unused)
+ *   q_turned    : [B, H_q, d] contiguous, 16-byte aligned: scratch for the rotated
+ *                 queries (NULL with rotary = 0)
+ *   seqlens     : whole lengths, the new key among them (positions[b] + 1)
+ *   prefix_table, workspace, workspace_bytes: as for sha_decode_prefix; with
+ *                 prefix_len = 0 not used
+ * Everything else as in the calls it stands for.
+ */
+sha_status_t sha_append_decode_paged(
+    const void *q, const int64_t q_strides[2], const void *k, const int64_t k_strides[2],
+    const void *v, const int64_t v_strides[2], void *k_pages, void *v_pages,
+    const int32_t *block_table, const int32_t *batch_head_index, const int32_t *positions,
+    const int32_t *seqlens, const double *inv_freq, int rotary, int interleaved, float mscale,
+    void *q_turned, const int32_t *prefix_table, int prefix_len, int B, int H_q, int H_kv,
+    int num_pages, int page_size, int max_pages, int d, int top_k, float scale, void *out,
+    sha_dtype_t dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * sha_get_device_status -- synchronises `stream`, then reads and clears the
  * current device's sticky flags: SHA_ERR_BAD_INDEX if any call since the last
  * read met an out-of-range head id, SHA_ERR_TIMEOUT if a pipeline wait gave

@@ -201,6 +201,81 @@ def test_refusals(sha):
         sha.append_decode_paged(s.fused[0].cuda()[:, :4], k, v, *args)
 
 
+@pytest.mark.parametrize("prefix_len", [0, 16])
+def test_a_refused_step_has_written_nothing(sha, prefix_len):
+    """Whatever is wrong with a step's arguments, and however late it is found: the cache, the
+    queries and the output stay as they were."""
+    s = Steps(2, 4, 2, 64, 1, 16, 2, 8, torch.float16, seed=9)
+    fused = s.fused[0].cuda()
+    q, k, v = fused.split([4, 2, 2], dim=1)
+    at = torch.full((2,), 16, dtype=torch.int32, device="cuda")
+    kp, vp = (torch.full_like(p, 5.0, device="cuda") for p in (s.k_pages, s.v_pages))
+    pt, freq = s.prefix_table.cuda(), s.freq.cuda()
+    out = torch.full((2, 4, 64), 9.0, dtype=torch.float16, device="cuda")
+    good = dict(q=q, k=k, v=v, k_pages=kp, v_pages=vp, batch_head_index=s.idx[0].cuda(),
+                positions=at, seqlens=at + 1, block_table=s.table.cuda(), inv_freq=freq,
+                prefix_len=prefix_len, prefix_table=pt, scale=0.125, out=out)
+    odd = torch.full((kp.shape[0], 2, 12, 64), 5.0, dtype=torch.float16, device="cuda")
+    refused = [
+        (ValueError, dict(batch_head_index=s.idx[0].cuda().long())),
+        (ValueError, dict(batch_head_index=s.idx[0].cuda()[:1])),
+        (ValueError, dict(seqlens=at[:1])), (ValueError, dict(seqlens=at.long())),
+        (ValueError, dict(block_table=s.table.cuda()[:1])), (ValueError, dict(positions=at.cpu())),
+        (ValueError, dict(out=out[:1])), (ValueError, dict(out=out.float())),
+        (ValueError, dict(out=out.cpu())), (ValueError, dict(inv_freq=freq.float())),
+        (ValueError, dict(inv_freq=None)), (ValueError, dict(prefix_len=-1)),
+        (ValueError, dict(workspace=torch.empty(1 << 24))), (ValueError, dict(v_pages=vp[1:])),
+        (ValueError, dict(prefix_len=17)), (ValueError, dict(prefix_len=16, prefix_table=None)),
+        (ValueError, dict(prefix_len=16, prefix_table=pt.long())),
+        (sha.ShaError, dict(scale=float("inf"))), (sha.ShaError, dict(mscale=float("nan"))),
+        (sha.ShaError, dict(k_pages=odd, v_pages=odd)),
+        (sha.ShaError, dict(batch_head_index=torch.zeros((2, 3), dtype=torch.int32,
+                                                         device="cuda"))),
+        (sha.ShaError, dict(prefix_len=80, prefix_table=torch.zeros(10, dtype=torch.int32,
+                                                                    device="cuda"))),
+        (sha.ShaError, dict(prefix_len=16, workspace=torch.empty(512, dtype=torch.uint8,
+                                                                 device="cuda"))),
+    ]
+    before = fused.clone()
+    for error, bad in refused:
+        with pytest.raises(error):
+            sha.append_decode_paged(**{**good, **bad})
+    torch.cuda.synchronize()
+    assert (kp == 5.0).all() and (vp == 5.0).all() and (odd == 5.0).all() and (out == 9.0).all()
+    assert torch.equal(fused, before)
+    assert sha.sha_get_device_status() == sha.SHA_OK
+    sha.append_decode_paged(**good)                       # and as it stands it is taken
+    assert sha.sha_get_device_status() == sha.SHA_OK
+    assert (kp != 5.0).any() and (out != 9.0).any()
+
+
+def test_steps_without_a_rotation(sha):
+    """Nothing turned: the queries are read where they are, and the keys appended as they are."""
+    B, H_q, H_kv, d, n = 3, 8, 2, 64, 20
+    g = torch.Generator().manual_seed(17)
+    kp, vp = (torch.full((2 * B, H_kv, 16, d), float("nan"), dtype=torch.float16, device="cuda")
+              for _ in range(2))
+    table = torch.randperm(2 * B, generator=g).reshape(B, 2).to(torch.int32).cuda()
+    idx = torch.tensor([[0, 1], [1, 0], [0, 1]], dtype=torch.int32, device="cuda")
+    qkv = torch.randn((n, B, H_q + 2 * H_kv, d), generator=g).half()
+    for t in range(n):
+        q, k, v = qkv[t].cuda().split([H_q, H_kv, H_kv], dim=1)
+        at = torch.full((B,), t, dtype=torch.int32, device="cuda")
+        out = sha.append_decode_paged(q.contiguous(), k, v, kp, vp, idx, at, at + 1, table)
+        assert out.shape == (B, H_q, d)
+    assert sha.sha_get_device_status() == sha.SHA_OK
+    q, k, v = qkv.double().split([H_q, H_kv, H_kv], dim=2)
+    for b in range(B):
+        for h in range(H_q):
+            w = torch.softmax(k[:, b, h // 4] @ q[-1, b, h] * d ** -0.5, dim=0)
+            want, A = w @ v[:, b, h // 4], w @ v[:, b, h // 4].abs()
+            S = d ** -0.5 * (q[-1, b, h].abs() @ k[:, b, h // 4].abs().T).max()
+            # the decode's bound (prefix_reference)
+            bound = 2.0 ** -11 * (want.abs() + A) + n * 2.0 ** -25 * v.abs().max() \
+                + A * (2 * (d + 2) * 2.0 ** -23 * S + 2.0 ** -20 + n * 2.0 ** -23)
+            assert ((out[b, h].cpu().double() - want).abs() <= bound).all()
+
+
 def test_waits_that_give_up(sha):
     """With the test build's wait limit at 1 ns the shared-prefix call's waits run out: it returns,
     reports the timeout, and the next call with the limit restored is right.  In a process of its
