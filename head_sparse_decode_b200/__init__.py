@@ -896,6 +896,23 @@ def _explain_append(k, v, k_pages, v_pages, block_table, positions, rows, inv_fr
 _lib.sha_append_decode_paged.argtypes = [_vp] * 13 + [_i, _i, _f, _vp, _vp] + [_i] * 9 + [
     _f, _vp, _i, _vp, ctypes.c_size_t, _vp]
 _lib.sha_append_decode_paged.restype = _i
+_lib.sha_append_decode_workspace_size.argtypes = [_i] * 7
+_lib.sha_append_decode_workspace_size.restype = ctypes.c_size_t
+
+
+@functools.lru_cache(maxsize=1024)
+def _step_workspace_size(B, H_q, H_kv, d, top_k, max_keys, prefix_len, index):
+    with torch.cuda.device(index):
+        return int(_lib.sha_append_decode_workspace_size(B, H_q, H_kv, d, top_k, max_keys,
+                                                         prefix_len))
+
+
+def append_decode_workspace_size(B, H_q, H_kv, d, top_k, max_keys, prefix_len=0, device=None):
+    """Workspace bytes append_decode_paged needs for these sizes on ``device`` (max_keys:
+    block_table's columns times the page size)."""
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        return _step_workspace_size(B, H_q, H_kv, d, top_k, max_keys, prefix_len,
+                                    torch.cuda.current_device())
 
 
 def append_decode_paged(q, k, v, k_pages, v_pages, batch_head_index, positions, seqlens,
@@ -909,8 +926,10 @@ def append_decode_paged(q, k, v, k_pages, v_pages, batch_head_index, positions, 
 
     q [B, H_q, d] and k, v [B, H_kv, d] are views with d contiguous (slices of a fused
     projection's rows); out [B, H_q, d] is new if not given, its unselected rows then
-    uninitialised.  Without inv_freq q must be contiguous.  A call that is refused has
-    written nothing."""
+    uninitialised.  Without inv_freq q must be contiguous.  workspace (default: a new
+    tensor) is uint8, at least append_decode_workspace_size bytes, with and without a
+    prefix; steps that share it must not overlap.  A call that is refused has written
+    nothing."""
     if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
         raise ValueError("q must be [B, H_q, d] and k [B, H_kv, d]")
     prefix_len = int(prefix_len)
@@ -956,10 +975,11 @@ def append_decode_paged(q, k, v, k_pages, v_pages, batch_head_index, positions, 
     if out is None:
         out = _made_for(stream, device,
                         lambda: torch.empty_like(q, memory_format=torch.contiguous_format))
-    if prefix_len > 0 and workspace is None:
-        nbytes = _prefix_workspace_size(B, H_q, H_kv, d, top_k, index)
+    if workspace is None:
+        nbytes = _step_workspace_size(B, H_q, H_kv, d, top_k, max_pages * pool[2],
+                                      1 if prefix_len else 0, index)
         workspace = _made_for(stream, device, lambda: seqlens.new_empty((nbytes + 3) // 4))
-    elif workspace is not None:
+    else:
         nbytes = workspace.numel() * workspace.element_size()
     _on_device(device, _lib.sha_append_decode_paged,
                (q.data_ptr(), _stride_pair(qs[0], qs[1]), k.data_ptr(), _stride_pair(ks[0], ks[1]),
@@ -970,7 +990,7 @@ def append_decode_paged(q, k, v, k_pages, v_pages, batch_head_index, positions, 
                 None if turned is None else turned.data_ptr(),
                 None if prefix_len == 0 else prefix_table.data_ptr(), prefix_len, B, H_q, H_kv,
                 pool[0], pool[2], max_pages, d, top_k, _default_scale(scale, d), out.data_ptr(),
-                code, None if workspace is None else workspace.data_ptr(), nbytes, handle))
+                code, workspace.data_ptr(), nbytes, handle))
     return out
 
 
@@ -1032,5 +1052,5 @@ __all__ = [
     "sha_copy_bandwidth_probe", "decode",
     "alloc_workspace", "ShaError", "LIBRARY_PATH", "sha_decode_noalloc",
     "rope_frequencies", "sha_rope", "sha_append_paged", "sha_decode_prefix",
-    "sha_decode_prefix_workspace_size", "append_decode_paged",
+    "sha_decode_prefix_workspace_size", "append_decode_paged", "append_decode_workspace_size",
 ]

@@ -998,7 +998,8 @@ sha_status_t paged_call(const void *q, const void *k_pages, const void *v_pages,
                         const int32_t *batch_head_index, const int32_t *seqlens,
                         const int32_t *block_table, int B, int H_q, int H_kv,
                         int num_pages, int page_size, int max_pages, int d, int top_k,
-                        float scale, void *out, sha_dtype_t dtype, void *stream, bool launch)
+                        float scale, void *out, sha_dtype_t dtype, void *workspace,
+                        size_t workspace_bytes, bool library_workspace, void *stream, bool launch)
 {
     if (num_pages < 1 || page_size < 1 || max_pages < 1) return SHA_ERR_INVALID_ARG;
     if ((long long)max_pages * page_size > (1 << 30)) return SHA_ERR_INVALID_ARG;
@@ -1012,8 +1013,8 @@ sha_status_t paged_call(const void *q, const void *k_pages, const void *v_pages,
     lay.max_pages = max_pages;
     lay.num_pages = num_pages;
     return decode_impl(q, k_pages, v_pages, batch_head_index, B, H_q, H_kv,
-                       max_pages * page_size, d, top_k, scale, out, dtype, nullptr, 0, 0,
-                       stream, true, lay, ForcedCluster(), launch);
+                       max_pages * page_size, d, top_k, scale, out, dtype, workspace,
+                       workspace_bytes, 0, stream, library_workspace, lay, ForcedCluster(), launch);
 }
 
 sha_status_t prefix_call(const void *q, const void *k_pages, const void *v_pages,
@@ -1153,7 +1154,7 @@ sha_status_t sha_append_call(      // sha_rope.cu: sha_append_paged, or its chec
     const int32_t *rows, const int32_t *positions, int B, int num_pages, int page_size,
     int max_pages, const double *inv_freq, int rotary, int interleaved, float mscale,
     const void *q, const int64_t q_strides[2], int H_q, void *q_out, const int64_t q_out_strides[2],
-    sha_dtype_t dtype, void *stream, bool launch);
+    sha_dtype_t dtype, void *stream, bool launch, int *clear, int clear_words);
 
 extern "C" {
 
@@ -1202,7 +1203,8 @@ sha_status_t sha_decode_paged(const void *q, const void *k_pages, const void *v_
                               float scale, void *out, sha_dtype_t dtype, void *stream)
 {
     return paged_call(q, k_pages, v_pages, batch_head_index, seqlens, block_table, B, H_q, H_kv,
-                      num_pages, page_size, max_pages, d, top_k, scale, out, dtype, stream, true);
+                      num_pages, page_size, max_pages, d, top_k, scale, out, dtype, nullptr, 0, true,
+                      stream, true);
 }
 
 sha_status_t sha_decode_strided(const void *q, const void *k, const void *v,
@@ -1263,6 +1265,19 @@ sha_status_t sha_decode_prefix(const void *q, const void *k_pages, const void *v
                        out, dtype, workspace, workspace_bytes, stream, true);
 }
 
+size_t sha_append_decode_workspace_size(int B, int H_q, int H_kv, int d, int top_k, int max_keys,
+                                        int prefix_len)
+{
+    if (prefix_len < 0) return 0;
+    if (prefix_len > 0) return sha_decode_prefix_workspace_size(B, H_q, H_kv, d, top_k);
+    if (check_shape(B, H_q, H_kv, max_keys, d, top_k, 1.0f) != SHA_OK || B == 0 || top_k == 0)
+        return 0;
+    int dev;
+    DeviceInfo *info;
+    if (current_device(&dev, &info) != SHA_OK) return 0;
+    return make_varlen_plan(B, H_q, H_kv, max_keys, d, top_k, 0, info->num_sms).workspace_bytes();
+}
+
 sha_status_t sha_append_decode_paged(
     const void *q, const int64_t q_strides[2], const void *k, const int64_t k_strides[2],
     const void *v, const int64_t v_strides[2], void *k_pages, void *v_pages,
@@ -1276,12 +1291,14 @@ sha_status_t sha_append_decode_paged(
     const int64_t rows[2] = {(int64_t)H_q * d, d};
     const bool turn = rotary > 0;
     const void *queries = turn ? q_turned : q;
+    int clear_words = 0;           // the paged decode's arrival counters: the append zeroes them
     // both calls' checks, then both calls
     for (const bool launch : {false, true}) {
         sha_status_t st = sha_append_call(
             k, v, k_strides, v_strides, B, H_kv, d, k_pages, v_pages, block_table, nullptr,
             positions, B, num_pages, page_size, max_pages, inv_freq, rotary, interleaved, mscale,
-            turn ? q : nullptr, q_strides, turn ? H_q : 0, q_turned, rows, dtype, stream, launch);
+            turn ? q : nullptr, q_strides, turn ? H_q : 0, q_turned, rows, dtype, stream, launch,
+            static_cast<int *>(workspace), clear_words);
         if (st == SHA_OK)
             st = prefix_len > 0
                      ? prefix_call(queries, k_pages, v_pages, batch_head_index, seqlens,
@@ -1290,8 +1307,17 @@ sha_status_t sha_append_decode_paged(
                                    workspace_bytes, stream, launch)
                      : paged_call(queries, k_pages, v_pages, batch_head_index, seqlens,
                                   block_table, B, H_q, H_kv, num_pages, page_size, max_pages, d,
-                                  top_k, scale, out, dtype, stream, launch);
+                                  top_k, scale, out, dtype, workspace, workspace_bytes, false,
+                                  stream, launch);
         if (st != SHA_OK) return st;
+        if (prefix_len == 0 && B > 0 && top_k > 0) {
+            int dev;
+            DeviceInfo *info;
+            st = current_device(&dev, &info);
+            if (st != SHA_OK) return st;
+            clear_words = make_varlen_plan(B, H_q, H_kv, max_pages * page_size, d, top_k, 0,
+                                           info->num_sms).sched.num_ctas;
+        }
     }
     return SHA_OK;
 }

@@ -168,14 +168,15 @@ extern "C" sha_status_t sha_rope(const void *x, const int32_t *positions, const 
 }
 
 // sha_append_paged, or (launch false) its checks alone: a step that appends and then
-// decodes launches nothing unless both calls' arguments hold.
+// decodes launches nothing unless both calls' arguments hold.  clear: words that the
+// launch sets to zero, too (RopeParams::clear).
 sha_status_t sha_append_call(
     const void *k, const void *v, const int64_t k_strides[2], const int64_t v_strides[2], int T,
     int H_kv, int d, void *k_pages, void *v_pages, const int32_t *block_table,
     const int32_t *rows, const int32_t *positions, int B, int num_pages, int page_size,
     int max_pages, const double *inv_freq, int rotary, int interleaved, float mscale,
     const void *q, const int64_t q_strides[2], int H_q, void *q_out, const int64_t q_out_strides[2],
-    sha_dtype_t dtype, void *stream, bool launch)
+    sha_dtype_t dtype, void *stream, bool launch, int *clear, int clear_words)
 {
     sha_status_t st = check_rotation(T, d, rotary, interleaved, mscale, dtype);
     if (st != SHA_OK) return st;
@@ -229,6 +230,8 @@ sha_status_t sha_append_call(
     p.d = d;
     p.rotary = rotary;
     p.mscale = mscale;
+    p.clear = clear;
+    p.clear_words = clear_words;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return dtype == SHA_FP16 ? run<__half>(p, interleaved, true, s)
                              : run<__nv_bfloat16>(p, interleaved, true, s);
@@ -245,5 +248,5 @@ extern "C" sha_status_t sha_append_paged(
     return sha_append_call(k, v, k_strides, v_strides, T, H_kv, d, k_pages, v_pages, block_table,
                            rows, positions, B, num_pages, page_size, max_pages, inv_freq, rotary,
                            interleaved, mscale, q, q_strides, H_q, q_out, q_out_strides, dtype,
-                           stream, true);
+                           stream, true, nullptr, 0);
 }

@@ -50,6 +50,8 @@ struct RopeParams {
     int T, B, num_pages, page_size, max_pages;
     int d, rotary;
     float mscale;
+    int *clear;                  // append: words set to zero for the stream's next kernel,
+    int clear_words;             // the arrival counters of a step's decode; or null
     int tok_per_block, heads_per_block, v_per_block;
 };
 
@@ -149,6 +151,8 @@ __global__ void __launch_bounds__(kRopeThreads) sha_rope_kernel(const RopeParams
         cs[i] = make_float2(c * p.mscale, s * p.mscale);
     }
     if constexpr (kAppend) {
+        if (p.clear && blockIdx.x == 0 && blockIdx.y == 0)
+            for (int i = tid; i < p.clear_words; i += kRopeThreads) p.clear[i] = 0;
         if (tid < toks) {
             const long long t = t0 + tid;
             const int pos = p.positions[t];

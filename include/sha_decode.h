@@ -505,8 +505,13 @@ sha_status_t sha_append_paged(const void *k, const void *v, const int64_t k_stri
  *   q_turned    : [B, H_q, d] contiguous, 16-byte aligned: scratch for the rotated
  *                 queries (NULL with rotary = 0)
  *   seqlens     : whole lengths, the new key among them (positions[b] + 1)
- *   prefix_table, workspace, workspace_bytes: as for sha_decode_prefix; with
- *                 prefix_len = 0 not used
+ *   prefix_table : as for sha_decode_prefix; with prefix_len = 0 not used
+ *   workspace   : device, 256-byte aligned, >= sha_append_decode_workspace_size
+ *                 bytes, with and without a prefix; scratch only (no contents
+ *                 carried between calls), owned by the caller; calls that share it
+ *                 must not overlap on the device.  The library's own workspace is
+ *                 not used: steps on several streams, or captured in several
+ *                 graphs, are independent if their workspaces are.
  * Everything else as in the calls it stands for.
  */
 sha_status_t sha_append_decode_paged(
@@ -517,6 +522,12 @@ sha_status_t sha_append_decode_paged(
     void *q_turned, const int32_t *prefix_table, int prefix_len, int B, int H_q, int H_kv,
     int num_pages, int page_size, int max_pages, int d, int top_k, float scale, void *out,
     sha_dtype_t dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace sha_append_decode_paged needs on the current device for rows of
+ * up to max_keys = max_pages * page_size keys; 0 for sizes it would reject and for
+ * empty calls. */
+size_t sha_append_decode_workspace_size(int B, int H_q, int H_kv, int d, int top_k, int max_keys,
+                                        int prefix_len);
 
 /*
  * sha_get_device_status -- synchronises `stream`, then reads and clears the

@@ -276,6 +276,89 @@ def test_steps_without_a_rotation(sha):
             assert ((out[b, h].cpu().double() - want).abs() <= bound).all()
 
 
+class Split:
+    """A step whose units are split over blocks and merged through the workspace: few rows, long
+    ones.  The keys lie in the cache already, as the step would write them."""
+
+    def __init__(self, B, H_q, H_kv, d, keys, seed):
+        g = torch.Generator().manual_seed(seed)
+        ps = 64
+        pages = -(-keys // ps)
+        mk = lambda *shape: torch.randn(shape, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+        self.kp, self.vp = mk(B * pages, H_kv, ps, d), mk(B * pages, H_kv, ps, d)
+        self.table = torch.randperm(B * pages, generator=g).reshape(B, pages).to(torch.int32).cuda()
+        self.q = mk(B, H_q, d)
+        at = torch.tensor([keys - 1 - 7 * b for b in range(B)])
+        rows = torch.arange(B, device="cuda")
+        page = self.table[rows, (at // ps).cuda()].long()
+        self.k, self.v = (p[page, :, (at % ps).cuda()].clone() for p in (self.kp, self.vp))
+        self.at = at.to(torch.int32).cuda()
+        self.idx = torch.arange(H_kv, dtype=torch.int32, device="cuda").expand(B, H_kv).contiguous()
+        self.lens = self.at + 1
+        self.sizes = (B, H_q, H_kv, d, H_kv, pages * ps)
+        self.out = torch.empty((B, H_q, d), dtype=torch.bfloat16, device="cuda")
+
+    def step(self, sha, **kw):
+        return sha.append_decode_paged(self.q, self.k, self.v, self.kp, self.vp, self.idx, self.at,
+                                       self.lens, self.table, out=self.out, **kw)
+
+    def want(self, sha):
+        """The same decode by itself."""
+        return sha.sha_decode_paged(self.q, self.kp, self.vp, self.idx, self.lens, self.table, None,
+                                    torch.empty_like(self.out))
+
+
+@pytest.mark.parametrize("H_q,H_kv", [(4, 4), (16, 2)])
+def test_a_step_without_a_prefix_takes_the_workspace_it_is_given(sha, H_q, H_kv):
+    """Whatever the workspace holds, within its bytes, and none that is too small."""
+    s = Split(2, H_q, H_kv, 128, 6000, seed=21)
+    want = s.want(sha)
+    need = sha.append_decode_workspace_size(*s.sizes)
+    ws = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        s.out.zero_()
+        s.step(sha, workspace=ws[:need])
+        assert torch.equal(s.out, want)
+        ws[:need].fill_(0xFF)
+    assert (ws[need:] == 0xA5).all()
+    with pytest.raises(sha.ShaError) as e:
+        s.step(sha, workspace=ws[:256])
+    assert e.value.status == sha.SHA_ERR_WORKSPACE
+    assert sha.sha_get_device_status() == sha.SHA_OK
+
+
+def test_steps_without_a_prefix_at_once(sha):
+    """Steps on two streams, each with a workspace of its own (given, or new), then captured in
+    two graphs that are replayed at once."""
+    steps = [Split(2, 16, 2, 128, 9000, seed=31), Split(3, 4, 4, 64, 7000, seed=32)]
+    wants = [s.want(sha).clone() for s in steps]
+    streams = [torch.cuda.Stream() for _ in steps]
+    spaces = [torch.empty(sha.append_decode_workspace_size(*s.sizes), dtype=torch.uint8,
+                          device="cuda") for s in steps]
+    torch.cuda.synchronize()
+    for given in (True, False):
+        for _ in range(20):
+            for s, stream, ws in zip(steps, streams, spaces):
+                s.step(sha, workspace=ws if given else None, stream=stream)
+        torch.cuda.synchronize()
+        for s, want in zip(steps, wants):
+            assert torch.equal(s.out, want)
+            s.out.zero_()
+    graphs = []
+    for s in steps:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            s.step(sha)
+    for _ in range(20):
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for s, want in zip(steps, wants):
+        assert torch.equal(s.out, want)
+    assert sha.sha_get_device_status() == sha.SHA_OK
+
+
 def test_waits_that_give_up(sha):
     """With the test build's wait limit at 1 ns the shared-prefix call's waits run out: it returns,
     reports the timeout, and the next call with the limit restored is right.  In a process of its

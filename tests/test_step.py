@@ -56,6 +56,14 @@ def test_host_checks_of_the_prefix_and_empty_steps(sha, kw, code):
     assert _step(sha, **kw) == code
 
 
+def test_workspace_sizes_of_sizes_it_would_reject(sha):
+    size = sha._lib.sha_append_decode_workspace_size
+    assert size(2, 8, 2, 64, 1, 0, 0) == 0                # no keys
+    assert size(2, 8, 2, 72, 1, 64, 0) == size(2, 9, 2, 64, 1, 64, 0) == 0
+    assert size(0, 8, 2, 64, 1, 64, 0) == size(2, 8, 2, 64, 0, 64, 0) == 0
+    assert size(2, 8, 2, 64, 1, 64, -1) == 0
+
+
 def test_python_refusals(sha):
     t = torch.zeros(2, 2, 64, dtype=torch.float16)
     i = torch.zeros(2, 1, dtype=torch.int32)
