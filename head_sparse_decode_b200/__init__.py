@@ -922,7 +922,9 @@ def append_decode_paged(q, k, v, k_pages, v_pages, batch_head_index, positions, 
     and value are appended at positions[b] (with inv_freq rotated, and the queries with
     them), then the selected heads attend to keys [0, seqlens[b]) -- seqlens counts the
     new key, so it is positions + 1.  With prefix_len > 0 the rows share the prefix in
-    prefix_table's pages (sha_decode_prefix), else sha_decode_paged runs.
+    prefix_table's pages (sha_decode_prefix), else sha_decode_paged runs.  A row without a
+    token (the padding of a captured batch) has positions[b] = -1 and seqlens[b] = 0; its
+    output stays as it was.
 
     q [B, H_q, d] and k, v [B, H_kv, d] are views with d contiguous (slices of a fused
     projection's rows); out [B, H_q, d] is new if not given, its unselected rows then

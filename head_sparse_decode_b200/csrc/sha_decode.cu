@@ -759,6 +759,7 @@ struct KvLayout {
     KvStrides k_strides{}, v_strides{};
     const int32_t *tokens = nullptr;        // head x token sparsity: [B, top_k, n_sel] (device)
     int n_sel = 0;
+    bool empty_rows = false;                // a length of 0 is no bad input
 };
 
 // N_kv is the padded length (per-row lengths) or max_pages * page_size (paged).
@@ -867,6 +868,7 @@ sha_status_t decode_impl(const void *q, const void *k, const void *v, const int3
     prm.batch_dim = 2;
     prm.tokens = lay.tokens;
     prm.n_sel = lay.n_sel;
+    prm.empty_rows = lay.empty_rows;
     if (lay.strided) {
         StridedMaps kv;
         int vt, vh, vb;
@@ -994,12 +996,14 @@ sha_status_t launch_prefix(const sha::PrefixParams &prm, const void *k, const vo
 }
 
 // sha_decode_paged and sha_decode_prefix, or (launch false) their checks alone.
+// empty_rows: a length of 0 is a row without a token, left alone without the flag.
 sha_status_t paged_call(const void *q, const void *k_pages, const void *v_pages,
                         const int32_t *batch_head_index, const int32_t *seqlens,
                         const int32_t *block_table, int B, int H_q, int H_kv,
                         int num_pages, int page_size, int max_pages, int d, int top_k,
                         float scale, void *out, sha_dtype_t dtype, void *workspace,
-                        size_t workspace_bytes, bool library_workspace, void *stream, bool launch)
+                        size_t workspace_bytes, bool library_workspace, void *stream, bool launch,
+                        bool empty_rows)
 {
     if (num_pages < 1 || page_size < 1 || max_pages < 1) return SHA_ERR_INVALID_ARG;
     if ((long long)max_pages * page_size > (1 << 30)) return SHA_ERR_INVALID_ARG;
@@ -1012,6 +1016,7 @@ sha_status_t paged_call(const void *q, const void *k_pages, const void *v_pages,
     lay.page_size = page_size;
     lay.max_pages = max_pages;
     lay.num_pages = num_pages;
+    lay.empty_rows = empty_rows;
     return decode_impl(q, k_pages, v_pages, batch_head_index, B, H_q, H_kv,
                        max_pages * page_size, d, top_k, scale, out, dtype, workspace,
                        workspace_bytes, 0, stream, library_workspace, lay, ForcedCluster(), launch);
@@ -1023,7 +1028,7 @@ sha_status_t prefix_call(const void *q, const void *k_pages, const void *v_pages
                          int prefix_len, int B, int H_q, int H_kv, int num_pages,
                          int page_size, int max_pages, int d, int top_k, float scale,
                          void *out, sha_dtype_t dtype, void *workspace,
-                         size_t workspace_bytes, void *stream, bool launch)
+                         size_t workspace_bytes, void *stream, bool launch, bool empty_rows)
 {
     if (dtype != SHA_FP16 && dtype != SHA_BF16) return SHA_ERR_UNSUPPORTED;
     if (num_pages < 1 || page_size < 1 || max_pages < 1 || prefix_len < 1) return SHA_ERR_INVALID_ARG;
@@ -1084,6 +1089,7 @@ sha_status_t prefix_call(const void *q, const void *k_pages, const void *v_pages
     suf.top_k = top_k;
     suf.min_len = prefix_len;
     suf.max_len = max_pages * page_size;
+    suf.empty_rows = empty_rows;
     // the last box boundary at or before the prefix's end
     const int box = page_size < sha::SuffixConfig<128>::kStage ? page_size
                                                                : sha::SuffixConfig<128>::kStage;
@@ -1204,7 +1210,7 @@ sha_status_t sha_decode_paged(const void *q, const void *k_pages, const void *v_
 {
     return paged_call(q, k_pages, v_pages, batch_head_index, seqlens, block_table, B, H_q, H_kv,
                       num_pages, page_size, max_pages, d, top_k, scale, out, dtype, nullptr, 0, true,
-                      stream, true);
+                      stream, true, false);
 }
 
 sha_status_t sha_decode_strided(const void *q, const void *k, const void *v,
@@ -1262,7 +1268,7 @@ sha_status_t sha_decode_prefix(const void *q, const void *k_pages, const void *v
 {
     return prefix_call(q, k_pages, v_pages, batch_head_index, seqlens, block_table, prefix_table,
                        prefix_len, B, H_q, H_kv, num_pages, page_size, max_pages, d, top_k, scale,
-                       out, dtype, workspace, workspace_bytes, stream, true);
+                       out, dtype, workspace, workspace_bytes, stream, true, false);
 }
 
 size_t sha_append_decode_workspace_size(int B, int H_q, int H_kv, int d, int top_k, int max_keys,
@@ -1304,11 +1310,11 @@ sha_status_t sha_append_decode_paged(
                      ? prefix_call(queries, k_pages, v_pages, batch_head_index, seqlens,
                                    block_table, prefix_table, prefix_len, B, H_q, H_kv, num_pages,
                                    page_size, max_pages, d, top_k, scale, out, dtype, workspace,
-                                   workspace_bytes, stream, launch)
+                                   workspace_bytes, stream, launch, true)
                      : paged_call(queries, k_pages, v_pages, batch_head_index, seqlens,
                                   block_table, B, H_q, H_kv, num_pages, page_size, max_pages, d,
                                   top_k, scale, out, dtype, workspace, workspace_bytes, false,
-                                  stream, launch);
+                                  stream, launch, true);
         if (st != SHA_OK) return st;
         if (prefix_len == 0 && B > 0 && top_k > 0) {
             int dev;

@@ -217,6 +217,7 @@ __global__ void __launch_bounds__(GqaConfig<D>::block_threads(kLook, kLayout == 
     Walk walk;
     if constexpr (kVarlen) {
         if (!varlen_plan<C::threads(kLook)>(p.seqlens, p.B, p.top_k, p.N_kv, C::kTile, gridDim.x,
+                                      p.empty_rows,
                                       reinterpret_cast<long long *>(smem + C::kPlanOffset), S,
                                       walk))
             return;

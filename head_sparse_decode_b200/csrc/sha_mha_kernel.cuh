@@ -68,6 +68,7 @@ struct DecodeParams {
     // u * n_sel + n_sel) of its head (positions in [0, N_kv))
     const int32_t *tokens;
     int n_sel;
+    bool empty_rows;         // per-row lengths: 0 marks a row without a token, not bad input
 };
 
 // How K/V of a unit are found: one padded [N_kv] block per (b, h) with every
@@ -213,6 +214,7 @@ __global__ void __launch_bounds__(MhaConfig<D>::threads(kLook), SHA_MHA_BLOCKS_P
     Walk walk;
     if constexpr (kVarlen) {
         if (!varlen_plan<C::threads(kLook)>(p.seqlens, p.B, p.top_k, p.N_kv, C::kTile, gridDim.x,
+                                      p.empty_rows,
                                       reinterpret_cast<long long *>(smem + C::kPlanOffset), S,
                                       walk))
             return;

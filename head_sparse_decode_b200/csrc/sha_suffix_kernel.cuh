@@ -42,6 +42,7 @@ struct SuffixParams {
     const int32_t *idx, *seqlens, *block_table;
     int B, H_q, H_kv, top_k;
     int min_len, max_len;        // valid row lengths: [P, max_pages * page_size]
+    bool empty_rows;             // a length of 0 marks a row without a token, not bad input
     int key0;                    // first key loaded: P rounded down to a TMA box
     int page_shift, max_pages, num_pages;    // pages of 2^page_shift keys
     float scale_log2;            // scale * log2(e)
@@ -184,9 +185,10 @@ __device__ __forceinline__ void suffix_totals(const SuffixParams &p, long long *
     long long sum = 0;
     int tmax = 0;
     for (int r = tid; r < p.B; r += NT) {
-        const int T = suffix_stages(p, p.seqlens[r], C::kStage);
+        const int len = p.seqlens[r], T = suffix_stages(p, len, C::kStage);
         if (T == 0) {
-            if (blockIdx.x == 0) atomicOr(&g_sha_status, kStatusBadIndex);
+            if (blockIdx.x == 0 && !(p.empty_rows && len == 0))
+                atomicOr(&g_sha_status, kStatusBadIndex);
         } else {
             sum += (long long)p.top_k * (T + C::kUnitCost);
             tmax = max(tmax, T);

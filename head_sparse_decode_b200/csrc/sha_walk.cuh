@@ -11,7 +11,9 @@
 // block-wide prefix sum over rows) finds the row, slot and tile at which this
 // block's range begins.  From there the walk only needs seqlens[b] of the
 // rows it reaches.  Rows with a length outside [1, N_max] hold no tiles; they
-// raise the bad-input flag and their outputs stay untouched.
+// raise the bad-input flag and their outputs stay untouched; with empty_rows a
+// length of 0 is a row without a token (the padding of a batch), left alone
+// without the flag.
 #pragma once
 
 #include "sha_device.cuh"
@@ -163,7 +165,8 @@ struct VarlenWalk {
 // this block has nothing to do.  scratch: shared, >= 2 * (NT/32) + 8 longs.
 template <int NT>
 __device__ bool varlen_plan(const int32_t *seqlens, int B, int top_k, int n_max, int tile,
-                            int max_blocks, long long *scratch, Schedule &S, VarlenWalk &w)
+                            int max_blocks, bool empty_rows, long long *scratch, Schedule &S,
+                            VarlenWalk &w)
 {
     constexpr int kWarps = NT / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -175,7 +178,8 @@ __device__ bool varlen_plan(const int32_t *seqlens, int B, int top_k, int n_max,
     for (int r = tid; r < B; r += NT) {
         const int len = seqlens[r];
         const int T = varlen_tiles(len, n_max, tile);
-        if (T == 0 && blockIdx.x == 0) atomicOr(&g_sha_status, kStatusBadIndex);
+        if (T == 0 && blockIdx.x == 0 && !(empty_rows && len == 0))
+            atomicOr(&g_sha_status, kStatusBadIndex);
         sum += (long long)top_k * T;
         tmax = max(tmax, T);
     }

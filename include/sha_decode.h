@@ -504,7 +504,11 @@ sha_status_t sha_append_paged(const void *k, const void *v, const int64_t k_stri
  *                 rotary = 0 q is contiguous and read as it is (q_strides unused)
  *   q_turned    : [B, H_q, d] contiguous, 16-byte aligned: scratch for the rotated
  *                 queries (NULL with rotary = 0)
- *   seqlens     : whole lengths, the new key among them (positions[b] + 1)
+ *   seqlens     : whole lengths, the new key among them (positions[b] + 1).  A row
+ *                 without a token (the padding of a captured batch) has position
+ *                 -1 and length 0: nothing else of it matters, its output stays as
+ *                 it was and nothing is flagged, unlike in the decodes by
+ *                 themselves, where a length of 0 is bad input.
  *   prefix_table : as for sha_decode_prefix; with prefix_len = 0 not used
  *   workspace   : device, 256-byte aligned, >= sha_append_decode_workspace_size
  *                 bytes, with and without a prefix; scratch only (no contents

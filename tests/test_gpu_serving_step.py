@@ -359,6 +359,72 @@ def test_steps_without_a_prefix_at_once(sha):
     assert sha.sha_get_device_status() == sha.SHA_OK
 
 
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("H_q,H_kv,d", [(8, 2, 128), (4, 4, 64)])
+def test_captured_step_with_padded_rows(sha, H_q, H_kv, d, shared):
+    """A step captured for six rows and replayed for fewer: rows without a token leave cache and
+    output as they were, raise no flag, and change nothing for the others."""
+    s = Steps(6, H_q, H_kv, d, 2, 40, 9, 8, torch.bfloat16, seed=18)
+    want = s.run(sha, shared)
+    dev = "cuda"
+    kp, vp = s.k_pages.to(dev), s.v_pages.to(dev)
+    table, pt, freq = s.table.to(dev), s.prefix_table.to(dev), s.freq.to(dev)
+    tables = [pt[None].contiguous()] if shared else [table[b:b + 1].contiguous() for b in range(6)]
+    for t in tables:
+        sha.sha_append_paged(s.prompt[0].to(dev), s.prompt[1].to(dev), kp, vp, t,
+                             torch.arange(40, dtype=torch.int32, device=dev),
+                             rows=torch.zeros(40, dtype=torch.int32, device=dev), inv_freq=freq)
+    fused = torch.zeros_like(s.fused[0], device=dev)
+    q, k, v = fused.split([H_q, H_kv, H_kv], dim=1)
+    idx = torch.zeros((6, 2), dtype=torch.int32, device=dev)
+    at = torch.full((6,), -1, dtype=torch.int32, device=dev)
+    lens = torch.zeros(6, dtype=torch.int32, device=dev)
+    rows_table = table.clone()
+    out = torch.empty((6, H_q, d), dtype=torch.bfloat16, device=dev)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        sha.append_decode_paged(q, k, v, kp, vp, idx, at, lens, rows_table, inv_freq=freq,
+                                prefix_len=40 if shared else 0, prefix_table=pt if shared else None,
+                                scale=d ** -0.5, out=out)
+    done = [0] * 6                                        # tokens that each row has
+    for rows in ([0, 1, 2, 3, 4, 5], [0, 2], [5], [], [1, 3, 4], [0, 1, 2, 3, 4, 5]):
+        fused.fill_(float("nan"))
+        # a padded row's token, head ids and pages do not matter
+        idx.fill_(-3 if len(rows) % 2 else 1)
+        rows_table.fill_(10 ** 6)
+        at.fill_(-1)
+        lens.zero_()
+        for b in rows:
+            fused[b].copy_(s.fused[done[b]][b])
+            idx[b].copy_(s.idx[done[b]][b])
+            rows_table[b].copy_(table[b])
+            at[b] = 40 + done[b]
+            lens[b] = 41 + done[b]
+        out.fill_(9.0)
+        graph.replay()
+        got = out.cpu()
+        assert sha.sha_get_device_status() == sha.SHA_OK
+        for b in range(6):
+            if b not in rows:
+                assert (got[b] == 9.0).all()
+                continue
+            # cut otherwise than in the full batch: equal up to the order of fp32 sums, and one
+            # rounding of the weights and of the output a side (the bound of `check`, twice)
+            w, t = want[done[b]][b].double(), done[b]
+            vals = torch.cat([s.prompt[1], torch.stack([s.split(i)[2][b] for i in range(t + 1)])])
+            assert ((got[b].double() - w).abs()
+                    <= 2 * 2.0 ** -8 * (w.abs() + vals.double().abs().max()) + 1e-4)[w != 9.0].all()
+            assert (got[b][want[t][b] == 9.0] == 9.0).all()
+            done[b] += 1
+    # by themselves the decodes take such a row for bad input
+    q = torch.zeros((6, H_q, d), dtype=torch.bfloat16, device=dev)
+    sha.sha_decode_paged(q, kp, vp, idx, lens * 0, table, 1.0, out)
+    assert sha.sha_get_device_status() == sha.SHA_ERR_BAD_INDEX
+    sha.sha_decode_prefix(q, kp, vp, idx, lens * 0, table, 40, pt, 1.0, out)
+    assert sha.sha_get_device_status() == sha.SHA_ERR_BAD_INDEX
+
+
 def test_waits_that_give_up(sha):
     """With the test build's wait limit at 1 ns the shared-prefix call's waits run out: it returns,
     reports the timeout, and the next call with the limit restored is right.  In a process of its
