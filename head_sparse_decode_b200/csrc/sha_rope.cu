@@ -109,16 +109,43 @@ sha_status_t check_rotation(int T, int d, int rotary, int interleaved, float msc
     return SHA_OK;
 }
 
-// A [T, H, d] view: strides of dimensions longer than one are checked.
+// Whether rows of d elements at a * s0 + b * s1 (a < n0, b < n1; s0, s1 >= d) are all
+// apart: at once where one dimension's extent fits the other's stride, else by the
+// nearest two rows for every difference along the shorter dimension.
+bool rows_lie_apart(int64_t s0, int64_t n0, int64_t s1, int64_t n1, int64_t d)
+{
+    const auto fits = [&](int64_t big, int64_t small, int64_t n) {
+        return small <= (big - d) / (n - 1);                  // small * (n - 1) + d <= big
+    };
+    if (fits(s0, s1, n1) || fits(s1, s0, n0)) return true;
+    if (n0 > n1) {
+        const int64_t s = s0, n = n0;
+        s0 = s1;
+        n0 = n1;
+        s1 = s;
+        n1 = n;
+    }
+    for (int64_t a = 1; a < n0; ++a) {
+        if (s0 > INT64_MAX / a) break;                        // past any address
+        const int64_t b = a * s0 / s1, left = a * s0 - b * s1;
+        if (b < n1 && left < d) return false;
+        if (b + 1 < n1 && s1 - left < d) return false;
+    }
+    return true;
+}
+
+// A [T, H, d] view: strides of dimensions longer than one are checked, and that the
+// rows of one that is written lie apart.
 sha_status_t check_view(const int64_t strides[2], int T, int H, int d, bool written)
 {
     for (int i = 0; i < 2; ++i) {
         if ((i == 0 ? T : H) <= 1) continue;
         if (strides[i] < 0) return SHA_ERR_INVALID_ARG;
         if (strides[i] % 8 != 0) return SHA_ERR_MISALIGNED;
-        // rows that are written lie apart
         if (written && strides[i] < d) return SHA_ERR_INVALID_ARG;
     }
+    if (written && T > 1 && H > 1 && !rows_lie_apart(strides[0], T, strides[1], H, d))
+        return SHA_ERR_INVALID_ARG;
     return SHA_OK;
 }
 
@@ -250,3 +277,11 @@ extern "C" sha_status_t sha_append_paged(
                            interleaved, mscale, q, q_strides, H_q, q_out, q_out_strides, dtype,
                            stream, true, nullptr, 0);
 }
+
+#ifdef SHA_TEST_HOOKS
+// Test builds only (not part of the ABI).
+extern "C" int sha_test_rows_lie_apart(int64_t s0, int64_t n0, int64_t s1, int64_t n1, int64_t d)
+{
+    return rows_lie_apart(s0, n0, s1, n1, d);
+}
+#endif

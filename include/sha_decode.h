@@ -439,9 +439,9 @@ sha_status_t sha_selective_mlp(const void *x, const void *W1t, const void *W2t,
  *     out1 = mscale * (x1 cos a - x2 sin a),  out2 = mscale * (x2 cos a + x1 sin a)
  *   x, out      : [T, H, d] views, d contiguous; element (t, h, e) of x is at
  *                 x + t*x_strides[0] + h*x_strides[1] + e (strides in elements,
- *                 host arrays of 2 int64, each >= 0 -- for out >= d -- and a
- *                 multiple of 8; the stride of a dimension of size 1 is not
- *                 used).  out may be x itself (the same pointer and strides);
+ *                 host arrays of 2 int64, each >= 0 -- for out >= d, and so that
+ *                 its rows do not overlap -- and a multiple of 8; the stride of a
+ *                 dimension of size 1 is not used).  out may be x itself (the same pointer and strides);
  *                 otherwise the two must not overlap.
  *   positions   : device, int32 [T].  Negative positions turn backwards:
  *                 rotating by -positions undoes a rotation (up to mscale^2), and

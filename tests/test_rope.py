@@ -1,6 +1,7 @@
 """Rotary tables, and what sha_rope and sha_append_paged refuse before any launch (CPU)."""
 import ctypes
 import math
+import random
 
 import pytest
 import torch
@@ -65,6 +66,34 @@ def _append(sha, k=P, v=P, ks=(128, 64), vs=(128, 64), T=3, H_kv=2, d=64, kp=P, 
 ])
 def test_append_host_checks(sha, kw, code):
     assert _append(sha, **kw) == code
+
+
+@pytest.mark.parametrize("T,H,s0,s1", [
+    (2, 2, 64, 64), (3, 2, 64, 72), (4, 3, 128, 192), (2, 4, 136, 192), (64, 40, 64, 64)])
+def test_outputs_whose_rows_overlap_are_refused(sha, T, H, s0, s1):
+    """Two rows that share elements have no one result."""
+    assert _rope(sha, T=T, H=H, xs=(0, 0), os=(s0, s1)) == 1
+    assert _append(sha, T=T, B=T, H_q=H, qs=(0, 0), qos=(s0, s1)) == 1
+
+
+def test_overlap_check_is_exact(sha):
+    """Against the rows' addresses, sorted; nested views and interleaved ones."""
+    from head_sparse_decode_b200 import build
+    lib = ctypes.CDLL(build.build_test_hooks())
+    lib.sha_test_rows_lie_apart.argtypes = [ctypes.c_int64] * 5
+    rng, seen = random.Random(3), []
+    for _ in range(20000):
+        T, H, d = rng.randint(2, 9), rng.randint(2, 9), rng.choice([8, 64])
+        s0, s1 = (8 * rng.randint(d // 8, 90) for _ in range(2))
+        rows = sorted(t * s0 + h * s1 for t in range(T) for h in range(H))
+        apart = all(y - x >= d for x, y in zip(rows, rows[1:]))
+        assert bool(lib.sha_test_rows_lie_apart(s0, T, s1, H, d)) == apart
+        nested = s0 >= s1 * (H - 1) + d or s1 >= s0 * (T - 1) + d
+        seen.append((apart, nested))
+    assert {(True, True), (True, False), (False, False)} == set(seen)
+    far = (1 << 62) // 8 * 8
+    assert lib.sha_test_rows_lie_apart(far, 3, far - 8, 3, 8)
+    assert not lib.sha_test_rows_lie_apart(far, 3, far - 8, 3, 16)
 
 
 def test_python_refusals(sha):
