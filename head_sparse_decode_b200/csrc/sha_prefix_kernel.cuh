@@ -39,9 +39,8 @@
 //     into registers, which frees it for the next step's product at once, and write
 //     P = 2^(S c - m), 16 bits wide (the type of the operands; the sums l stay fp32
 //     and add the unrounded P).  A row's reference m moves only when a step's
-//     maximum exceeds it by more than 2^8: the weights then stay below 256, any m is
-//     exact, and the accumulator in tensor memory is rescaled in a few steps instead
-//     of in all.
+//     maximum exceeds the last one by kPrefixSlack: any m is exact, and the
+//     accumulator in tensor memory is rescaled in a few steps instead of in all.
 // So a step's exponentials run beside the next step's S and the last one's P V.
 // (Steps of 128 keys leave P no columns of its own but S's: each product then waits
 // for the one before it and the exponentials for both, 4840 clocks for a tile of 256
@@ -139,9 +138,16 @@ struct PrefixConfig {
     static_assert(kTmemP + kStep <= kTmemO && kTmemO + 2 * D <= kTmemCols, "S, P and O fit");
 };
 
-// A row's reference m moves when a tile's maximum exceeds it by more than this
-// (log2 units): P stays below 2^8, far inside fp16.
-constexpr float kPrefixSlack = 8.f;
+// A row's reference m moves when a step's maximum exceeds the one it was taken from by
+// more than the slack (log2 units), and lies the lift below that one.  fp16 weights so
+// use the type's upper exponents, too (up to 2^15), and are rounded by at most 2^-36 of
+// the largest; with m the maximum itself that is 2^-25, below which they were lost, and
+// many such keys together are not small beside one key's output.  bf16 has the exponents
+// of fp32.
+template <typename T>
+constexpr float kPrefixSlack = std::is_same<T, __half>::value ? 4.f : 8.f;
+template <typename T>
+constexpr float kPrefixLift = std::is_same<T, __half>::value ? 11.f : 0.f;
 
 // First row tile of every head (start[H_kv] = all of them), and how many row tiles
 // of more than 128 rows come before it (pairs[H_kv] = all of those), from the
@@ -847,9 +853,9 @@ __global__ void __launch_bounds__(PrefixConfig<D>::kThreads, 1)
                 }
                 if (ok && busy) {
                     // the first step sets the reference, later ones move it rarely
-                    const bool move = step == 0 || top > m_ref + kPrefixSlack;
+                    const bool move = step == 0 || top > m_ref + (kPrefixSlack<T> + kPrefixLift<T>);
                     if (__any_sync(FULL, move)) {
-                        const float m_new = move ? top : m_ref;
+                        const float m_new = move ? top - kPrefixLift<T> : m_ref;
                         if (step > 0) {
                             const float a = move ? exp2_approx(m_ref - m_new) : 1.f;
                             l0 *= a;

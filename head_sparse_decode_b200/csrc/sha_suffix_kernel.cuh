@@ -268,6 +268,12 @@ __device__ __forceinline__ bool suffix_plan(const SuffixParams &p, long long tot
     }
 }
 
+// The softmax's reference lies this far below the running maximum (log2 units): fp16
+// weights, up to 2^15, use the type's upper exponents, too, and are rounded by at most
+// 2^-40 of the largest instead of 2^-25.  bf16 has the exponents of fp32.
+template <typename T>
+constexpr float kSuffixLift = std::is_same<T, __half>::value ? 15.f : 0.f;
+
 // An 8 x 8 tile of 16-bit elements, one packed pair per lane, transposed.
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x)
 {
@@ -470,7 +476,7 @@ __device__ __forceinline__ void suffix_worker(const SuffixParams &p, const CUten
                     mt[r] = fmaxf(mt[r], __shfl_xor_sync(FULL, mt[r], 4));
                     mt[r] = fmaxf(mt[r], __shfl_xor_sync(FULL, mt[r], 8));
                     mt[r] = fmaxf(mt[r], __shfl_xor_sync(FULL, mt[r], 16));
-                    const float m_new = fmaxf(m_run[nt][r], mt[r]);
+                    const float m_new = fmaxf(m_run[nt][r], mt[r] - kSuffixLift<T>);
                     ref[r] = m_new == -INFINITY ? 0.f : m_new;
                     alpha[r] = exp2_approx(m_run[nt][r] - ref[r]);
                     m_run[nt][r] = m_new;

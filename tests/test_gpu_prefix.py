@@ -1,4 +1,6 @@
 """Shared-prefix decode on the GPU (sha_decode_prefix) against its definition in 64 bits."""
+import math
+
 import pytest
 import torch
 
@@ -90,6 +92,38 @@ def test_long_runs_that_end_in_a_short_tile(sha, B, H_q, H_kv, d, top_k, prefix,
     first = _check(sha, c)
     for _ in range(5):
         assert torch.equal(_run(sha, c), first)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("H_q,H_kv,d,prefix,suffix,sink", [
+    (4, 4, 128, 9000, 40, 17), (16, 1, 64, 9000, 40, 8999), (2, 2, 64, 40, 6000, 40),
+    (8, 1, 128, 3000, 3000, 0), (32, 2, 128, 200, 7000, 7199)])
+def test_many_small_weights_beside_a_large_one(sha, H_q, H_kv, d, prefix, suffix, sink, dtype):
+    """One key takes nearly all the weight and has the value 0; the others, each below 2^-25 of
+    it, together make the output."""
+    c = Case(2, H_q, H_kv, d, H_kv, prefix, suffix, 64, dtype, seed=45)
+    n = prefix + suffix
+    u = torch.randn(d, generator=torch.Generator().manual_seed(6)).sign()
+    c.q[:] = u.to(c.dtype)
+    for pool in (c.k_pages, c.v_pages):
+        pool[~torch.isnan(pool)] = 0.0 if pool is c.k_pages else 1.0
+    page = c.prefix_table[sink // 64] if sink < prefix else c.table[1, sink // 64]
+    c.k_pages[int(page), :, sink % 64] = u.to(c.dtype)
+    c.v_pages[int(page), :, sink % 64] = 0.0
+    c.idx, c.lens[0] = c.idx.sort(dim=1).values, prefix
+    scale = 18.0 / d                                      # the sink's score; the others' is 0
+    out = _run(sha, c, scale)[1].cpu().double()
+    assert sha.sha_get_device_status() == sha.SHA_OK
+    w = math.exp(-18.0)                                   # 2^-25.97
+    want = (n - 1) * w / (1.0 + (n - 1) * w)
+    # the output's rounding (the least fp16 here is normal) and the weights', half a step each,
+    # fp16 weights by up to 2^-36 of the largest where they are subnormal; exp2 2^-21, twice; the
+    # score in log2 units, 26, off by two roundings of the scale; sums of n terms, 2^-23 a step
+    u = {"fp16": 2.0 ** -11, "bf16": 2.0 ** -8}[dtype]
+    bound = want * (2 * u + 2.0 ** -20 + 40 * 2.0 ** -24 + n * 2.0 ** -23)
+    if dtype == "fp16":
+        bound += n * 2.0 ** -36
+    assert ((out - want).abs() <= bound).all()
 
 
 @pytest.mark.parametrize("args", SEVERAL_ROW_TILES, ids=str)
