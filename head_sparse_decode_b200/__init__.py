@@ -284,7 +284,10 @@ def sha_decode_prefix(q, k_pages, v_pages, batch_head_index, seqlens, block_tabl
     attention over the shared keys, which lie in the pages of prefix_table (int32
     [ceil(prefix_len / page_size)]), is computed once per KV head for all the rows that
     select it.  seqlens (int32 [B], each >= prefix_len) are whole lengths; block_table
-    rows cover the whole sequences, their entries for the prefix unread.  workspace
+    rows cover the whole sequences, their entries before prefix_len // page_size unread
+    (where a prefix ends inside a page, that page's entry is read, even for a row that
+    ends with the prefix).  With few rows a head or a few hundred shared keys
+    sha_decode_paged is faster (include/sha_decode.h has times).  workspace
     (default: a new tensor) is uint8, at least sha_decode_prefix_workspace_size bytes;
     calls that share it must not overlap."""
     prefix_len = int(prefix_len)
@@ -922,7 +925,9 @@ def append_decode_paged(q, k, v, k_pages, v_pages, batch_head_index, positions, 
     and value are appended at positions[b] (with inv_freq rotated, and the queries with
     them), then the selected heads attend to keys [0, seqlens[b]) -- seqlens counts the
     new key, so it is positions + 1.  With prefix_len > 0 the rows share the prefix in
-    prefix_table's pages (sha_decode_prefix), else sha_decode_paged runs.  A row without a
+    prefix_table's pages (sha_decode_prefix), else sha_decode_paged runs; where that is
+    the faster one (few rows, short prefixes) and the block tables reach every key of the
+    prefix, prefix_len = 0 may be given.  A row without a
     token (the padding of a captured batch) has positions[b] = -1 and seqlens[b] = 0; its
     output stays as it was.
 

@@ -329,8 +329,7 @@ struct PrefixCut {
 // the slower of the two parts is done first, out of 32 evenly spaced ones, one per
 // lane of the calling warp.  Times in ns, measured: a run's beginning and end; a key
 // tile of 128 keys by up to 128 rows, and by more; a worker's beginning; an SM's
-// share of a weight of the suffix (32 keys' bytes, per 64 elements of d).  The choice is
-// flat around them: 20 % more or less on any moved no case by more than 1 %.
+// share of a weight of the suffix (32 keys' bytes, per 64 elements of d).
 constexpr float kPrefixRunNs = 10000.f, kPrefixTileNs = 1600.f, kPrefixWideNs = 2450.f;
 constexpr float kSuffixRunNs = 5000.f, kSuffixWeightNs = 100.f;
 
